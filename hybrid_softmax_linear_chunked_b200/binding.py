@@ -7,6 +7,7 @@ library's CUDA kernels.  There is no CPU fallback: without the built library eve
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -29,7 +30,9 @@ EXPORTED = ["rehyat_last_error", "rehyat_version", "rehyat_featmap",
             "rehyat_forward_train", "rehyat_backward_workspace_size", "rehyat_backward",
             "rehyat_gemm_bf16", "rehyat_segment_workspace_size", "rehyat_segment_states",
             "rehyat_segment_attend", "rehyat_selftest_wait_timeout", "rehyat_selftest_bounds",
-            "rehyat_sync_status", "rehyat_debug_bounds"]
+            "rehyat_sync_status", "rehyat_debug_bounds", "rehyat_rotary",
+            "rehyat_decay_workspace_size", "rehyat_decay_forward", "rehyat_decay_backward",
+            "rehyat_decay_step"]
 
 
 class RehyatError(RuntimeError):
@@ -41,6 +44,24 @@ class RehyatError(RuntimeError):
 class Dims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("D", ctypes.c_int), ("F", ctypes.c_int),
                 ("G", ctypes.c_int), ("P", ctypes.c_int), ("phi", ctypes.c_int)]
+
+
+class Strides(ctypes.Structure):
+    """Elements between two sequences, heads and rows of a [B, heads, N, D] tensor."""
+    _fields_ = [("batch", ctypes.c_longlong), ("head", ctypes.c_longlong),
+                ("row", ctypes.c_longlong)]
+
+
+class RotaryArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "n", "Hq", "Hk", "D", "R", "interleaved",
+                                            "inverse", "axes", "pos64", "add_index")] + \
+        [(n, ctypes.c_longlong) for n in ("pos_axis", "pos_batch", "pos_token", "start")] + \
+        [("scale", ctypes.c_float)]
+
+
+class DecayArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "H", "Hk", "N", "D")] + \
+        [("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -114,6 +135,14 @@ def load() -> ctypes.CDLL:
     L.rehyat_selftest_wait_timeout.argtypes = [ctypes.c_longlong, P]
     L.rehyat_selftest_bounds.argtypes = [P, ctypes.c_longlong, ctypes.c_longlong, P]
     L.rehyat_debug_bounds.argtypes = []
+    SP = [P, Strides]  # a strided tensor
+    L.rehyat_rotary.argtypes = [RotaryArgs, c_int] + SP * 2 + [P, P, P] + SP * 2 + [P]
+    L.rehyat_decay_workspace_size.argtypes = [DecayArgs, c_int, c_int, ctypes.POINTER(c_size_t)]
+    L.rehyat_decay_forward.argtypes = [DecayArgs, c_int] + SP * 3 + [P, P, P] + SP + \
+        [P, P, c_size_t, P]
+    L.rehyat_decay_backward.argtypes = [DecayArgs, c_int] + SP * 3 + [P, P, P] + SP + [P] + \
+        SP * 3 + [P, P, c_size_t, P]
+    L.rehyat_decay_step.argtypes = [DecayArgs, c_int] + SP * 3 + [P, P, c_int, P] + SP + [P]
     L.rehyat_sync_status.argtypes = [P]
     for name in EXPORTED:
         if name not in ("rehyat_last_error",):
@@ -627,3 +656,292 @@ def sync_status(device: torch.device | None = None) -> None:
     """Synchronise the current stream and raise if a kernel reported a device-side failure."""
     dev = device or torch.device("cuda", torch.cuda.current_device())
     _check(load().rehyat_sync_status(_stream(dev)))
+
+
+# ---- rotary positions and linear attention with a decay per head ----
+# These calls read tensors by their strides: [B, heads, N, D] with contiguous rows of D, so a
+# transposed [B, N, heads, D] projection or a slice of a packed qkv needs no copy.
+
+def _strided(t: torch.Tensor, dev: torch.device, dtype: torch.dtype, shape, what: str):
+    """(pointer, strides) of a [B, heads, N, D] tensor for the library."""
+    if t.device != dev or dev.type != "cuda":
+        raise ValueError("all tensors must be on the same CUDA device")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[3] != 1 and shape[3] > 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    return t.data_ptr(), Strides(st[0], st[1], st[2])
+
+
+def _small(t: torch.Tensor | None, dev: torch.device, dtype: torch.dtype, shape, what: str):
+    """Pointer of an optional contiguous tensor of the given type and shape."""
+    if t is None:
+        return None
+    if t.device != dev:
+        raise ValueError("all tensors must be on the same CUDA device")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _scratch(nbytes: int, dev: torch.device, workspace: torch.Tensor | None) -> torch.Tensor:
+    if workspace is not None and (workspace.device != dev or workspace.dtype != torch.uint8 or
+                                  not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous uint8 tensor on the tensors' device")
+    return _workspace(nbytes, dev, workspace)
+
+
+def _call(dev: torch.device, fn, *args) -> None:
+    """Enqueue a library call on the current stream of the tensors' device, whichever device is
+    the current one."""
+    stream = ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, stream)
+    if status:
+        _check(status)
+
+
+def _four(t: torch.Tensor, what: str):
+    if t.dim() != 4:
+        raise ValueError(f"{what} must be [B, heads, N, D], got {tuple(t.shape)}")
+    return t.shape
+
+
+def rotary_frequencies(R: int, *, base: float = 10000.0, scaling: str | None = None,
+                       factor: float = 1.0, original_length: int | None = None,
+                       turns: tuple[float, float] = (32.0, 1.0),
+                       device: torch.device | None = None) -> tuple[torch.Tensor, float]:
+    """(freq, scale) for `rotary`: radians per position of the R/2 pairs (fp64), base^(-2p/R), and
+    the factor on the rotated values.  A context stretched by `factor`:
+      scaling "linear": every frequency divided by the factor;
+      scaling "ntk":    the base times factor^(R/(R-2)), so the slowest pair stretches by the
+                        factor and the fastest not at all;
+      scaling "yarn":   pairs that make at least turns[0] turns over `original_length` positions are
+                        kept, those with at most turns[1] divided by the factor, a linear ramp over
+                        the pair index between; values times 0.1 ln(factor) + 1."""
+    if R < 2 or R % 2:
+        raise ValueError(f"R={R} must be even and positive")
+    if not factor >= 1.0 or not base > 1.0:
+        raise ValueError(f"need factor >= 1 and base > 1 (factor={factor}, base={base})")
+    scale = 1.0
+    if scaling == "ntk":
+        if R == 2:
+            raise ValueError("scaling 'ntk' needs R > 2")
+        base = base * factor ** (R / (R - 2))
+    p = torch.arange(R // 2, dtype=torch.float64)
+    freq = base ** (-2.0 * p / R)
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "yarn":
+        if original_length is None or original_length < 1 or not turns[0] > turns[1] > 0:
+            raise ValueError("scaling 'yarn' needs original_length and turns[0] > turns[1] > 0")
+        lo, hi = (R * math.log(original_length / (t * 2 * math.pi)) / (2 * math.log(base))
+                  for t in turns)
+        lo, hi = max(math.floor(lo), 0), min(math.ceil(hi), R - 1)
+        keep = 1 - ((p - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        freq = freq * keep + freq / factor * (1 - keep)
+        scale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return freq.to(device), scale
+
+
+def rotary_axes(pairs: tuple[int, ...], device: torch.device | None = None) -> torch.Tensor:
+    """The `axis` argument of `rotary`: the first pairs[0] pairs turn by axis 0, the next pairs[1]
+    by axis 1, and so on."""
+    return torch.repeat_interleave(torch.arange(len(pairs), dtype=torch.uint8),
+                                   torch.tensor(pairs)).to(device)
+
+
+def video_positions(T: int, frame_h: int, frame_w: int, *, first_frame: int = 0,
+                    device: torch.device | None = None) -> torch.Tensor:
+    """positions [3, 1, T*frame_h*frame_w] (frame, row, column) of a frame-major token sequence;
+    expand the middle dimension to the batch."""
+    i = torch.arange(T * frame_h * frame_w, device=device)
+    L = frame_h * frame_w
+    return torch.stack((first_frame + i // L, i // frame_w % frame_h, i % frame_w))[:, None].to(
+        torch.int32)
+
+
+def rotary(q: torch.Tensor, k: torch.Tensor | None, freq: torch.Tensor, *,
+           positions: torch.Tensor | None = None, start=0, axis: torch.Tensor | None = None,
+           scale: float = 1.0, interleaved: bool = False, inverse: bool = False,
+           q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None):
+    """Rotary positions for q [B,H,n,D] and k [B,Hk,n,D] (or None) in one launch: dimension pairs
+    of the first R = 2 len(freq) dimensions turn by position * freq[pair] and are scaled by `scale`;
+    the rest is copied.  Pairs are (p, p + R/2), or (2p, 2p + 1) when interleaved.
+
+    Token i of sequence b has position positions[b, i] ([B, n]) or, pair by pair,
+    positions[axis[pair], b, i] ([A, B, n], axis [R/2] uint8); without `positions`, i.  `start` (an
+    int, or without `positions` an int32/int64 tensor [B] on the device) is added.  Positions are
+    int32 or int64 tensors of any strides; an axis past the last counts as the last.
+
+    inverse turns the other way: with the same arguments it is the gradient of this call.  Returns
+    q_out, or (q_out, k_out); they may be q and k (in place)."""
+    lib = load()
+    B, H, n, D = _four(q, "q")
+    dev, dtype = q.device, q.dtype
+    code = _dtype_code(q)
+    qp, qs = _strided(q, dev, dtype, q.shape, "q")
+    R = 2 * freq.numel()
+    fp = _small(freq, dev, torch.float64, (R // 2,), "freq")
+    a = RotaryArgs(B, n, H, 0, D, R, int(interleaved), int(inverse), 1, 0, 0, 0, 0, 0, 0, scale)
+    pos = positions
+    if isinstance(start, torch.Tensor):
+        if positions is not None:
+            raise ValueError("give positions or a start tensor, not both")
+        if start.shape != (B,):
+            raise ValueError(f"start must have shape {(B,)}, got {tuple(start.shape)}")
+        pos, a.pos_batch, a.add_index = start, start.stride(0), 1
+    elif positions is None:
+        a.start, a.add_index = start, 1
+    else:
+        a.start = start
+        st = positions.stride()
+        if positions.shape == (B, n):
+            a.pos_batch, a.pos_token = st
+        elif positions.dim() == 3 and positions.shape[1:] == (B, n):
+            a.axes, (a.pos_axis, a.pos_batch, a.pos_token) = positions.shape[0], st
+        else:
+            raise ValueError(f"positions must have shape {(B, n)} or (axes, {B}, {n}), got "
+                             f"{tuple(positions.shape)}")
+    if pos is not None:
+        if pos.device != dev:
+            raise ValueError("all tensors must be on the same CUDA device")
+        if pos.dtype not in (torch.int32, torch.int64):
+            raise TypeError(f"positions must be int32 or int64, got {pos.dtype}")
+        a.pos64 = int(pos.dtype == torch.int64)
+    ap = _small(axis, dev, torch.uint8, (R // 2,), "axis")
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    qop, qos = _strided(q_out, dev, dtype, q.shape, "q_out")
+    kp = kop = None
+    ks = kos = Strides()
+    if k is not None:
+        _four(k, "k")
+        a.Hk = k.shape[1]
+        kp, ks = _strided(k, dev, dtype, (B, a.Hk, n, D), "k")
+        if k_out is None:
+            k_out = torch.empty_like(k)
+        kop, kos = _strided(k_out, dev, dtype, k.shape, "k_out")
+    _call(dev, lib.rehyat_rotary, a, code, qp, qs, kp, ks, fp, ap,
+          None if pos is None else pos.data_ptr(), qop, qos, kop, kos)
+    return q_out if k is None else (q_out, k_out)
+
+
+def _decay_args(q, k, scale: float) -> DecayArgs:
+    B, H, N, D = _four(q, "q")
+    Hk = _four(k, "k")[1]
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"k's {Hk} heads must divide q's {H}")
+    return DecayArgs(B, H, Hk, N, D, scale)
+
+
+def decay_workspace_size(a: DecayArgs, dtype_code: int, backward: bool = False) -> int:
+    n = ctypes.c_size_t(0)
+    status = load().rehyat_decay_workspace_size(a, dtype_code, int(backward), ctypes.byref(n))
+    if status:
+        _check(status)
+    return n.value
+
+
+def decay_forward(q, k, v, log_decay, *, scale: float = 1.0, lengths: torch.Tensor | None = None,
+                  state: torch.Tensor | None = None, final_state: bool | torch.Tensor = False,
+                  out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Linear attention with a decay L = exp(log_decay[h]) per head over a whole prompt:
+      out_i = scale * (sum_{j<=i} L^(i-j) (q_i . k_j) v_j + L^(i+1) q_i state)
+    q [B,H,N,D]; k, v [B,Hk,N,D] (H a multiple of Hk; query head h reads key/value head
+    h // (H/Hk)); bf16 or fp32; D a multiple of 8 up to 128; log_decay [H] fp32, constants <= 0.
+    lengths [B] int32: sequence b is its first lengths[b] rows, the others are padding (not read
+    into any result, zero in the output).  state [B,H,D,D] fp32: from the rows before.
+    final_state True: returns (out, the state after the last row [B,H,D,D] fp32), which
+    `decay_step` or the next call goes on from; a tensor: written there (it may be `state`)."""
+    lib = load()
+    a = _decay_args(q, k, scale)
+    dev, dtype, code = q.device, q.dtype, _dtype_code(q)
+    kv = (a.B, a.Hk, a.N, a.D)
+    square = (a.B, a.H, a.D, a.D)
+    qa, ka, va = (_strided(q, dev, dtype, q.shape, "q"), _strided(k, dev, dtype, kv, "k"),
+                  _strided(v, dev, dtype, kv, "v"))
+    gp = _small(log_decay, dev, torch.float32, (a.H,), "log_decay")
+    lp = _small(lengths, dev, torch.int32, (a.B,), "lengths")
+    sp = _small(state, dev, torch.float32, square, "state")
+    if out is None:
+        out = torch.empty_like(q)
+    oa = _strided(out, dev, dtype, q.shape, "out")
+    last = None
+    if isinstance(final_state, torch.Tensor):
+        last = final_state
+    elif final_state:
+        last = torch.empty(square, dtype=torch.float32, device=dev)
+    fp = _small(last, dev, torch.float32, square, "final_state")
+    ws = _scratch(decay_workspace_size(a, code), dev, workspace)
+    _call(dev, lib.rehyat_decay_forward, a, code, *qa, *ka, *va, gp, lp, sp, *oa, fp,
+          ws.data_ptr(), ws.numel())
+    return out if last is None else (out, last)
+
+
+def decay_backward(q, k, v, log_decay, dout, *, scale: float = 1.0,
+                   lengths: torch.Tensor | None = None, state: torch.Tensor | None = None,
+                   dfinal: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None) -> dict:
+    """Gradients of sum(dout * out) + sum(dfinal * final state) of `decay_forward`: dict with dq
+    [B,H,N,D], dk, dv [B,Hk,N,D] (the inputs' type; dk and dv summed over the query heads that share
+    them; zero on padding) and, with `state`, dstate [B,H,D,D] fp32.  dout [B,H,N,D]; dfinal
+    [B,H,D,D] fp32 or None (zero)."""
+    lib = load()
+    a = _decay_args(q, k, scale)
+    dev, dtype, code = q.device, q.dtype, _dtype_code(q)
+    kv = (a.B, a.Hk, a.N, a.D)
+    square = (a.B, a.H, a.D, a.D)
+    qa, ka, va, doa = (_strided(q, dev, dtype, q.shape, "q"), _strided(k, dev, dtype, kv, "k"),
+                       _strided(v, dev, dtype, kv, "v"),
+                       _strided(dout, dev, dtype, q.shape, "dout"))
+    gp = _small(log_decay, dev, torch.float32, (a.H,), "log_decay")
+    lp = _small(lengths, dev, torch.int32, (a.B,), "lengths")
+    sp = _small(state, dev, torch.float32, square, "state")
+    fp = _small(dfinal, dev, torch.float32, square, "dfinal")
+    g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v)}
+    if state is not None:
+        g["dstate"] = torch.empty(square, dtype=torch.float32, device=dev)
+    outs = [x for n in ("dq", "dk", "dv") for x in _strided(g[n], dev, dtype, g[n].shape, n)]
+    ws = _scratch(decay_workspace_size(a, code, True), dev, workspace)
+    _call(dev, lib.rehyat_decay_backward, a, code, *qa, *ka, *va, gp, lp, sp, *doa, fp, *outs,
+          g["dstate"].data_ptr() if state is not None else None, ws.data_ptr(), ws.numel())
+    return g
+
+
+def decay_step(q, k, v, log_decay, state, *, scale: float = 1.0,
+               slots: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """One token of every sequence: state <- L state + k v^T (in place), out = scale * q state.
+    q [B,H,1,D]; k, v [B,Hk,1,D]; state [pool,H,D,D] fp32.  slots [B] int32: sequence b's state
+    is state[slots[b]] (without slots: state[b], pool = B); a negative slot is an idle entry (zero
+    output, no state touched); a slot listed several times takes its tokens in batch order; one past
+    the pool gives zeros and is reported by `sync_status`."""
+    lib = load()
+    a = _decay_args(q, k, scale)
+    if a.N != 1:
+        raise ValueError(f"a step takes one token of each sequence, got {a.N}")
+    dev, dtype, code = q.device, q.dtype, _dtype_code(q)
+    kv = (a.B, a.Hk, 1, a.D)
+    pool = state.shape[0] if slots is not None and state.dim() == 4 else a.B
+    qa, ka, va = (_strided(q, dev, dtype, q.shape, "q"), _strided(k, dev, dtype, kv, "k"),
+                  _strided(v, dev, dtype, kv, "v"))
+    gp = _small(log_decay, dev, torch.float32, (a.H,), "log_decay")
+    sp = _small(state, dev, torch.float32, (pool, a.H, a.D, a.D), "state")
+    lp = _small(slots, dev, torch.int32, (a.B,), "slots")
+    if out is None:
+        out = torch.empty_like(q)
+    oa = _strided(out, dev, dtype, q.shape, "out")
+    _call(dev, lib.rehyat_decay_step, a, code, *qa, *ka, *va, gp, sp, pool, lp, *oa)
+    return out

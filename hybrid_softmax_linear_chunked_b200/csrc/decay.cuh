@@ -1,0 +1,532 @@
+// Linear attention with a decay L = exp(log_decay[h]) per head, CUDA-core kernels: fp32 prompts and
+// gradients, the scan that joins segments (fp32 and bf16), the single-token step, and the sum over
+// query heads that share a key/value head.
+//
+// One form serves the prompt and its gradients.  A pass reads rows a, b, c and writes
+//     out_i = sp * sum_{j in past(i)} L^|i-j| (a_i . b_j) c_j  +  si * L^(t_i + e) a_i^T S ,
+//     S    <- L^n S + sd * sum_j L^(n - t_j - e) b_j c_j^T              (over the n rows of a range)
+// where past(i) is j <= i and t_i = i - (first row of the range) forward in time, j >= i and
+// t_i = (last row) - i backward.  With the rows q, k, v, dO and the state S:
+//     prompt  out: a = q,  b = k,  c = v   forward,  e = 1, S from S_0
+//     dQ         : a = dO, b = v,  c = k   forward,  e = 1, S^T
+//     dK         : a = v,  b = dO, c = q   backward, e = 0, dS^T   (from the final state's gradient)
+//     dV         : a = k,  b = q,  c = dO  backward, e = 0, dS
+// e says on which side of a range's border the state stands: S_0 has decayed once when row 0 reads
+// it, the gradient of the last state reaches the last row undecayed.
+//
+// A sequence is cut into segments of whole 128-row blocks.  Three launches: the sum of every
+// segment's own rows (decay_states), its exclusive prefix in time order (decay_scan), and the rows
+// of every segment, chunk after chunk with the state carried along (decay_rows).  Every exponent
+// above is >= 0, so no power grows for L <= 1 and none is divided by; L = 0 (log_decay = -inf)
+// leaves each row its own term.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "sm100.cuh"
+
+namespace rehyat {
+namespace decay {
+
+constexpr int kMaxD = 128;
+constexpr int kBlockRows = 128;  // segments start at multiples of this
+constexpr int kC = 64;           // rows of one chunk of the CUDA-core kernels
+constexpr int kThreads = 256;
+
+// Rows of a [B, heads, N, D] tensor with strides in elements; head h of the pass reads head
+// h / group (query heads that share a key/value head).
+struct Rows {
+  const void* p;
+  long long sb, sh, sn;
+  int group;
+};
+
+struct Pass {
+  Rows a, b, c;
+  void* out;                 // row type, or fp32 where the group sum follows
+  long long ob, oh, on;      // its strides
+  const float* log_decay;    // [H]
+  const int* lengths;        // [B] or null: rows at and past a sequence's length are padding
+  const float* prefix;       // [B*H][nseg][D][D] state before each segment in time, or null (zero)
+  float* delta;              // [B*H][nseg][D][D] each segment's own sum (written by the states)
+  int B, H, N, D;
+  int nseg, seg_rows;
+  int reverse, e;
+  int transposed;            // the pass's state is the transpose of `prefix`
+  int seg_skip;              // states: the segment whose sum nothing reads, or -1
+  float sp, si, sd;
+};
+
+// log2 of the decay, bounded below so that 0 * log2(0) stays 0 (2^-1000 is 0 in fp32); NaN stays.
+__device__ __forceinline__ float log2_decay(const float* g, int h) {
+  const float x = g[h] * 1.4426950408889634f;
+  return x < -1000.f ? -1000.f : x;
+}
+__device__ __forceinline__ int length_of(const int* lengths, int b, int N) {
+  return lengths ? min(max(lengths[b], 0), N) : N;
+}
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) {
+  return *reinterpret_cast<const float4*>(p);
+}
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+  const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+  return make_float4(x.x, x.y, y.x, y.y);
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(sm100::pack_bf16x2(v.x, v.y), sm100::pack_bf16x2(v.z, v.w));
+}
+
+__device__ __forceinline__ float4 fma4(float s, float4 v, float4 acc) {
+  return make_float4(fmaf(s, v.x, acc.x), fmaf(s, v.y, acc.y), fmaf(s, v.z, acc.z),
+                     fmaf(s, v.w, acc.w));
+}
+__device__ __forceinline__ float4 mul4(float s, float4 v) {
+  return make_float4(s * v.x, s * v.y, s * v.z, s * v.w);
+}
+
+// Rows [r0, r0 + kC) of one head into shared memory as fp32 [kC][ld], columns [D, Dp) and rows at
+// or past `end` as zeros whatever the tensor holds there.
+template <typename T>
+__device__ __forceinline__ void load_rows(float* dst, int ld, const Rows& t, int b, int h, int r0,
+                                          int end, int D, int Dp) {
+  const T* src = static_cast<const T*>(t.p) + b * t.sb + (h / t.group) * t.sh;
+  const int v4 = Dp / 4;
+  for (int i = threadIdx.x; i < kC * v4; i += kThreads) {
+    const int r = i / v4, c = (i - r * v4) * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r0 + r < end && c < D) x = load4<T>(src + (long long)(r0 + r) * t.sn + c);
+    *reinterpret_cast<float4*>(dst + r * ld + c) = x;
+  }
+}
+
+// Shared memory of the CUDA-core kernels in floats: tiles have rows of Dp + 4 (Dp = D rounded up
+// to 32), so that threads of a warp on different rows reach different banks.
+__host__ __device__ constexpr int padded(int D) { return (D + 31) / 32 * 32; }
+__host__ __device__ constexpr int rows_smem_floats(int Dp) {
+  return 3 * kC * (Dp + 4) + kC * (kC + 4) + Dp * (Dp + 4);
+}
+__host__ __device__ constexpr int states_smem_floats(int Dp) { return 2 * kC * (Dp + 4); }
+
+// acc[8][8] += sum_r (w[r] x[r][i0 + 8]) y[r][j0 + 8]^T over the kC rows of two tiles; the thread's
+// rows are i0 .. i0+3, i0+64 .. (half apart) and columns likewise, so a warp's float4 reads fall
+// on neighbouring banks.
+struct Outer {
+  int i0, j0, half;
+  bool on;
+};
+__device__ __forceinline__ Outer outer_of(int Dp) {
+  // (Dp / 8)^2 threads hold 8 x 8 elements each
+  const int n = Dp / 8;
+  Outer o;
+  o.on = threadIdx.x < n * n;
+  o.i0 = (threadIdx.x / n) * 4;
+  o.j0 = (threadIdx.x % n) * 4;
+  o.half = Dp / 2;
+  return o;
+}
+__device__ __forceinline__ void outer_add(float4 (&acc)[8][2], const float* x, const float* y,
+                                          int ld, const Outer& o, float g2, int last_time,
+                                          int first_row, int sign, float sd, int rows) {
+  // weight of row r: sd * L^(last_time - sign * (first_row + r))
+#pragma unroll 2
+  for (int r = 0; r < rows; ++r) {
+    const float w = sd * exp2f(g2 * (float)(last_time - sign * (first_row + r)));
+    const float4 x0 = *reinterpret_cast<const float4*>(x + r * ld + o.i0);
+    const float4 x1 = *reinterpret_cast<const float4*>(x + r * ld + o.i0 + o.half);
+    const float4 y0 = mul4(w, *reinterpret_cast<const float4*>(y + r * ld + o.j0));
+    const float4 y1 = mul4(w, *reinterpret_cast<const float4*>(y + r * ld + o.j0 + o.half));
+    const float xs[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      acc[i][0] = fma4(xs[i], y0, acc[i][0]);
+      acc[i][1] = fma4(xs[i], y1, acc[i][1]);
+    }
+  }
+}
+__device__ __forceinline__ int outer_row(const Outer& o, int i) {
+  return i < 4 ? o.i0 + i : o.i0 + o.half + i - 4;
+}
+
+// Each segment's own sum: delta = sd * sum_j L^(n - t_j - e) b_j c_j^T over its n valid rows.
+// grid (nseg, B*H), block 256.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1) decay_states_kernel(const Pass p) {
+  extern __shared__ __align__(16) float smf[];
+  const int seg = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh - b * p.H;
+  if (seg == p.seg_skip) return;
+  const int Dp = padded(p.D), ld = Dp + 4;
+  float* sb = smf;
+  float* sc = sb + kC * ld;
+  const float g2 = log2_decay(p.log_decay, h);
+  const int r_begin = seg * p.seg_rows;
+  const int r_end = min(r_begin + p.seg_rows, length_of(p.lengths, b, p.N));
+  const Outer o = outer_of(Dp);
+  float4 acc[8][2];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int r0 = r_begin; r0 < r_end; r0 += kC) {
+    __syncthreads();
+    load_rows<T>(sb, ld, p.b, b, h, r0, r_end, p.D, Dp);
+    load_rows<T>(sc, ld, p.c, b, h, r0, r_end, p.D, Dp);
+    __syncthreads();
+    const int rows = min(kC, r_end - r0);
+    if (o.on) {
+      // forward: exponent r_end - 1 - r + (1 - e); backward: r - r_begin + (1 - e)
+      if (p.reverse)
+        outer_add(acc, sb, sc, ld, o, g2, 1 - p.e - r_begin, r0, -1, p.sd, rows);
+      else
+        outer_add(acc, sb, sc, ld, o, g2, r_end - p.e, r0, 1, p.sd, rows);
+    }
+  }
+  if (!o.on) return;
+  float* dst = p.delta + ((size_t)bh * p.nseg + seg) * p.D * p.D;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = outer_row(o, i);
+    if (r >= p.D) continue;
+    if (o.j0 < p.D) store4(dst + (size_t)r * p.D + o.j0, acc[i][0]);
+    if (o.j0 + o.half < p.D) store4(dst + (size_t)r * p.D + o.j0 + o.half, acc[i][1]);
+  }
+}
+
+// The state before each segment in time order, written over the segment's own sum, and the state
+// after the last: state_{s+1} = L^(rows of s) state_s + delta_s.  S0 and last may be the same
+// buffer (each element is read before it is written, by one thread).
+// grid (ceil(D*D/4 / 256), B*H), block 256.
+__global__ void __launch_bounds__(256)
+    decay_scan_kernel(float* delta, const float* S0, float* last, const float* log_decay,
+                      const int* lengths, int H, int N, int D, int nseg, int seg_rows, int reverse,
+                      int need_prefix) {
+  sm100::grid_dep_signal();
+  const int bh = blockIdx.y, b = bh / H, h = bh - b * H;
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  const int n4 = D * D / 4;
+  sm100::grid_dep_wait();
+  if (i >= n4) return;
+  const float g2 = log2_decay(log_decay, h);
+  const int n = length_of(lengths, b, N);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (S0) acc = reinterpret_cast<const float4*>(S0)[(size_t)bh * n4 + i];
+  float4* d = reinterpret_cast<float4*>(delta) + (size_t)bh * nseg * n4 + i;
+  const int steps = last ? nseg : nseg - 1;  // the last segment's sum is only in the last state
+#pragma unroll 4
+  for (int t = 0; t < nseg; ++t) {
+    const int s = reverse ? nseg - 1 - t : t;
+    const int rows = min(max(n - s * seg_rows, 0), seg_rows);
+    float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (t < steps && rows > 0) add = d[(size_t)s * n4];
+    if (need_prefix) d[(size_t)s * n4] = acc;
+    if (t < steps && rows > 0) acc = fma4(exp2f(g2 * (float)rows), acc, add);
+  }
+  if (last) reinterpret_cast<float4*>(last)[(size_t)bh * n4 + i] = acc;
+}
+
+// The rows of one segment: chunks of kC in time order, the state [D][D] carried in shared memory.
+// Bound by the fp32 pipes: 2 kC D (kC + 2 D) multiply-adds a chunk.
+// grid (nseg, B*H), block 256.
+template <typename T, typename TOut>
+__global__ void __launch_bounds__(kThreads, 1) decay_rows_kernel(const Pass p) {
+  extern __shared__ __align__(16) float smf[];
+  const int seg = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh - b * p.H;
+  const int Dp = padded(p.D), ld = Dp + 4, ldp = kC + 4;
+  float* sa = smf;
+  float* sb = sa + kC * ld;
+  float* sc = sb + kC * ld;
+  float* sp = sc + kC * ld;
+  float* ss = sp + kC * ldp;
+  const int tid = threadIdx.x;
+  const float g2 = log2_decay(p.log_decay, h);
+  const int n = length_of(p.lengths, b, p.N);
+  const int r_begin = seg * p.seg_rows, r_stop = min(r_begin + p.seg_rows, p.N);
+  const int r_end = min(r_stop, n);
+  TOut* out = static_cast<TOut*>(p.out) + b * p.ob + h * p.oh;
+
+  for (int i = tid; i < Dp * (Dp / 4); i += kThreads) {
+    const int r = i / (Dp / 4), c = (i - r * (Dp / 4)) * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.prefix && r < p.D && c < p.D) {
+      const float* src = p.prefix + ((size_t)bh * p.nseg + seg) * p.D * p.D;
+      if (p.transposed)
+        x = make_float4(src[(size_t)c * p.D + r], src[(size_t)(c + 1) * p.D + r],
+                        src[(size_t)(c + 2) * p.D + r], src[(size_t)(c + 3) * p.D + r]);
+      else
+        x = load4<float>(src + (size_t)r * p.D + c);
+    }
+    *reinterpret_cast<float4*>(ss + r * ld + c) = x;
+  }
+  const Outer o = outer_of(Dp);
+  const int nc = (r_stop - r_begin + kC - 1) / kC;
+  const int v4 = Dp / 4;
+  // output tile: 16 groups of 4 rows x (Dp / 8) columns of 8 (as 4 + 4, half apart)
+  const int ncol = Dp / 8;
+  const bool o_on = tid < 16 * ncol;
+  const int orow = (tid / ncol) * 4, ocol = (tid % ncol) * 4, ohalf = Dp / 2;
+  for (int ci = 0; ci < nc; ++ci) {
+    const int r0 = r_begin + (p.reverse ? nc - 1 - ci : ci) * kC;
+    const int rows = min(max(r_end - r0, 0), kC);  // valid rows
+    __syncthreads();
+    if (rows == 0) {  // nothing but padding: zeros, the state stays
+      for (int i = tid; i < kC * v4; i += kThreads) {
+        const int r = i / v4, c = (i - r * v4) * 4;
+        if (r0 + r < r_stop && c < p.D)
+          store4(out + (long long)(r0 + r) * p.on + c, make_float4(0.f, 0.f, 0.f, 0.f));
+      }
+      continue;
+    }
+    load_rows<T>(sa, ld, p.a, b, h, r0, r_end, p.D, Dp);
+    load_rows<T>(sb, ld, p.b, b, h, r0, r_end, p.D, Dp);
+    load_rows<T>(sc, ld, p.c, b, h, r0, r_end, p.D, Dp);
+    __syncthreads();
+    {  // P = sp * L^|i-j| (a_i . b_j) over the past of i, 4 x 4 a thread (columns 16 apart)
+      const int i0 = (tid / 16) * 4, j0 = tid % 16;
+      float acc[4][4] = {};
+      for (int k = 0; k < Dp; k += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          x[u] = *reinterpret_cast<const float4*>(sa + (i0 + u) * ld + k);
+          y[u] = *reinterpret_cast<const float4*>(sb + (j0 + 16 * u) * ld + k);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            acc[u][w] = fmaf(x[u].x, y[w].x, fmaf(x[u].y, y[w].y,
+                        fmaf(x[u].z, y[w].z, fmaf(x[u].w, y[w].w, acc[u][w]))));
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int i = i0 + u, j = j0 + 16 * w;
+          const int d = p.reverse ? j - i : i - j;
+          sp[i * ldp + j] =
+              d >= 0 && j < rows ? p.sp * exp2f(g2 * (float)d) * acc[u][w] : 0.f;
+        }
+    }
+    __syncthreads();
+    if (o_on) {  // out = si * L^(t + e) a^T S + P c
+      float4 acc[4][2];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) acc[u][0] = acc[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < Dp; k += 4) {
+        float4 x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const float4*>(sa + (orow + u) * ld + k);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float4 y0 = *reinterpret_cast<const float4*>(ss + (k + w) * ld + ocol);
+          const float4 y1 = *reinterpret_cast<const float4*>(ss + (k + w) * ld + ocol + ohalf);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float xv = w == 0 ? x[u].x : w == 1 ? x[u].y : w == 2 ? x[u].z : x[u].w;
+            acc[u][0] = fma4(xv, y0, acc[u][0]);
+            acc[u][1] = fma4(xv, y1, acc[u][1]);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int t = p.reverse ? rows - 1 - (orow + u) : orow + u;
+        const float f = p.si * exp2f(g2 * (float)(max(t, 0) + p.e));
+        acc[u][0] = mul4(f, acc[u][0]);
+        acc[u][1] = mul4(f, acc[u][1]);
+      }
+      for (int k = 0; k < kC; k += 4) {
+        float4 x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const float4*>(sp + (orow + u) * ldp + k);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float4 y0 = *reinterpret_cast<const float4*>(sc + (k + w) * ld + ocol);
+          const float4 y1 = *reinterpret_cast<const float4*>(sc + (k + w) * ld + ocol + ohalf);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float xv = w == 0 ? x[u].x : w == 1 ? x[u].y : w == 2 ? x[u].z : x[u].w;
+            acc[u][0] = fma4(xv, y0, acc[u][0]);
+            acc[u][1] = fma4(xv, y1, acc[u][1]);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int r = orow + u;
+        if (r0 + r >= r_stop) continue;
+        if (r >= rows) acc[u][0] = acc[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        TOut* dst = out + (long long)(r0 + r) * p.on;
+        if (ocol < p.D) store4(dst + ocol, acc[u][0]);
+        if (ocol + ohalf < p.D) store4(dst + ocol + ohalf, acc[u][1]);
+      }
+    }
+    __syncthreads();
+    if (ci + 1 < nc && o.on) {  // S = L^rows S + sd * sum L^(rows - t - e) b c^T
+      const float keep = exp2f(g2 * (float)rows);
+      float4 acc[8][2];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float* s = ss + outer_row(o, i) * ld;
+        acc[i][0] = mul4(keep, *reinterpret_cast<const float4*>(s + o.j0));
+        acc[i][1] = mul4(keep, *reinterpret_cast<const float4*>(s + o.j0 + o.half));
+      }
+      if (p.reverse)
+        outer_add(acc, sb, sc, ld, o, g2, 1 - p.e, 0, -1, p.sd, rows);
+      else
+        outer_add(acc, sb, sc, ld, o, g2, rows - p.e, 0, 1, p.sd, rows);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float* s = ss + outer_row(o, i) * ld;
+        *reinterpret_cast<float4*>(s + o.j0) = acc[i][0];
+        *reinterpret_cast<float4*>(s + o.j0 + o.half) = acc[i][1];
+      }
+    }
+  }
+}
+
+// out[b, kv head, row] = sum over its `group` query heads of part [B][Hk * group][N][D] (fp32),
+// in head order.  grid (blocks over rows * D / 4, B*Hk), block 256.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    decay_group_sum_kernel(const float* part, T* out, long long ob, long long oh, long long on,
+                           int Hk, int group, int N, int D) {
+  const int bk = blockIdx.y, b = bk / Hk, hk = bk - b * Hk;
+  const int v4 = D / 4;
+  const long long total = (long long)N * v4;
+  const float4* src = reinterpret_cast<const float4*>(part) + (long long)bk * group * total;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total;
+       i += (long long)gridDim.x * 256) {
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int u = 0; u < group; ++u) acc = fma4(1.f, src[u * total + i], acc);
+    const long long r = i / v4;
+    store4(out + b * ob + hk * oh + r * on + (i - r * v4) * 4, acc);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// One token: S <- L S + k v^T, o = scale * q S.
+// ---------------------------------------------------------------------------------------------
+struct StepParams {
+  Rows q, k, v;            // sn unused (one row); k and v grouped
+  void* out;
+  long long ob, oh;
+  const float* log_decay;
+  float* state;            // [pool][H][D][D]
+  const int* slots;        // [B] or null (sequence b's state is b)
+  int B, H, D, pool;
+  float scale;
+};
+
+// The state is read and written once (8 D^2 bytes a head and sequence), which bounds the step.  A
+// CTA owns kStepCols columns of one state: eight lanes cover a row's 128 bytes, 16 rows a pass, so
+// all its loads are in flight at once and no CTA waits on another.
+// A slot that a batch lists more than once is stepped in batch order: the CTA of its first entry
+// holds the state in registers and takes the later entries' tokens too.  A negative slot is an
+// idle entry (zeros out).  A slot past the pool is reported through the device error word.
+// grid (ceil(D / kStepCols), H, B), block 128.
+constexpr int kStepCols = 32, kStepThreads = 128;
+
+template <typename T, int kPasses>
+__global__ void __launch_bounds__(kStepThreads) decay_step_kernel(const StepParams p) {
+  __shared__ float sq[kMaxD], sk[kMaxD];
+  __shared__ float red[kStepThreads / 32][kStepCols];
+  __shared__ int next_sh;
+  const int tid = threadIdx.x, lane8 = tid & 7, row0 = tid >> 3;
+  const int col = blockIdx.x * kStepCols + lane8 * 4;
+  const int h = blockIdx.y;
+  int b = blockIdx.z;
+  const int D = p.D;
+  const bool col_ok = col < D;
+  const int slot = p.slots ? p.slots[b] : b;
+  if (slot < 0 || slot >= p.pool) {
+    if (slot >= p.pool && tid == 0 && atomicCAS(&sm100::g_device_error, 0, 2) == 0) {
+      sm100::g_bounds_info[0] = 50;
+      sm100::g_bounds_info[1] = slot;
+      sm100::g_bounds_info[2] = p.pool;
+    }
+    if (row0 == 0 && col_ok)
+      store4(static_cast<T*>(p.out) + b * p.ob + h * p.oh + col, make_float4(0.f, 0.f, 0.f, 0.f));
+    return;
+  }
+  float* S = p.state + ((size_t)slot * p.H + h) * D * D + col;
+  float4 s[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = row0 + 16 * i;
+    s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < D && col_ok) s[i] = *reinterpret_cast<const float4*>(S + (size_t)r * D);
+  }
+  if (p.slots) {  // an earlier entry of the same slot takes this one too
+    bool earlier = false;
+    for (int j = tid; j < b; j += kStepThreads) earlier |= p.slots[j] == slot;
+    if (__syncthreads_or(earlier)) return;
+  }
+  const float L = expf(p.log_decay[h]);
+  while (true) {
+    if (tid < D / 4) {
+      const T* q = static_cast<const T*>(p.q.p) + b * p.q.sb + (h / p.q.group) * p.q.sh + tid * 4;
+      *reinterpret_cast<float4*>(sq + tid * 4) = load4<T>(q);
+    } else if (tid >= 64 && tid < 64 + D / 4) {
+      const int c = (tid - 64) * 4;
+      const T* k = static_cast<const T*>(p.k.p) + b * p.k.sb + (h / p.k.group) * p.k.sh + c;
+      *reinterpret_cast<float4*>(sk + c) = load4<T>(k);
+    }
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (col_ok)
+      v = load4<T>(static_cast<const T*>(p.v.p) + b * p.v.sb + (h / p.v.group) * p.v.sh + col);
+    if (tid == 0) next_sh = p.B;
+    __syncthreads();
+    if (p.slots)
+      for (int j = b + 1 + tid; j < p.B; j += kStepThreads)
+        if (p.slots[j] == slot) {
+          atomicMin(&next_sh, j);
+          break;
+        }
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int r = row0 + 16 * i;
+      if (r < D) {
+        s[i] = fma4(sk[r], v, mul4(L, s[i]));
+        o = fma4(sq[r], s[i], o);
+      }
+    }
+#pragma unroll
+    for (int m = 8; m < 32; m <<= 1) {
+      o.x += __shfl_xor_sync(0xffffffffu, o.x, m);
+      o.y += __shfl_xor_sync(0xffffffffu, o.y, m);
+      o.z += __shfl_xor_sync(0xffffffffu, o.z, m);
+      o.w += __shfl_xor_sync(0xffffffffu, o.w, m);
+    }
+    if ((tid & 31) < 8) *reinterpret_cast<float4*>(&red[tid >> 5][lane8 * 4]) = o;
+    __syncthreads();
+    if (tid < 8 && col_ok) {
+      float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kStepThreads / 32; ++w)
+        t = fma4(1.f, *reinterpret_cast<const float4*>(&red[w][tid * 4]), t);
+      store4(static_cast<T*>(p.out) + b * p.ob + h * p.oh + col, mul4(p.scale, t));
+    }
+    b = next_sh;
+    if (b >= p.B) break;
+    __syncthreads();  // red, sq, sk and next_sh are written again
+  }
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = row0 + 16 * i;
+    if (r < D && col_ok) *reinterpret_cast<float4*>(S + (size_t)r * D) = s[i];
+  }
+}
+
+}  // namespace decay
+}  // namespace rehyat

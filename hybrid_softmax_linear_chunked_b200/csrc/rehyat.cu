@@ -1739,3 +1739,5 @@ int rehyat_sync_status(void* stream) {
 }
 
 }  // extern "C"
+
+#include "sequence_ops.cuh"

@@ -1,0 +1,198 @@
+// Rotary positions: pair p of a head's first R dimensions turns by the angle pos * freq[p],
+//     (x1, x2) -> scale * (x1 cos a - x2 sin a, x2 cos a + x1 sin a),
+// with (x1, x2) = (x[p], x[p + R/2]) (halves) or (x[2p], x[2p + 1]) (interleaved); dimensions R
+// and up are copied.  The gradient is the same turn by -a.
+//
+// Angles: a float holds pos * freq only to 2^-24 of its value, which at position 10^6 is 0.06
+// radians.  So a frequency is kept as a 64-bit fraction of a turn, and pos * freq modulo one turn is
+// an integer product that wraps: exact for every 64-bit position.  The wrapped turn's upper 32 bits
+// give the angle to 1.5e-9 radians, and sincospif its sine and cosine.
+//
+// Bound by memory: every row is read and written once.  A thread owns eight pairs of one token:
+// it forms their sines and cosines once, in registers, and applies them to every head of both
+// tensors, two 16-byte loads and stores (bf16) a head, so the trigonometry is a 1/(H + Hk) share.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "decay.cuh"
+
+namespace rehyat {
+namespace rotary {
+
+constexpr int kThreads = 128;
+constexpr int kPairs = 8;   // pairs a thread turns
+constexpr int kMaxAxes = 4;
+
+struct Tensor {
+  const void* x;
+  void* y;
+  long long xb, xh, xn, yb, yh, yn;  // strides in elements
+  int heads;
+};
+
+struct Params {
+  Tensor t[2];
+  int B, n, D, R;
+  int interleaved;
+  int copy_tail;               // dimensions R .. D-1 are copied (out of place)
+  const double* freq;          // [R/2] radians per position
+  const unsigned char* axis;   // [R/2] or null (all 0)
+  const void* pos;             // int32 or int64, or null
+  int pos64, axes;
+  long long pa, pb, pn;        // strides of pos: axis, sequence, token
+  int add_index;               // position = pos + token index
+  long long start;             // added to every position
+  float scale;
+  float sign;                  // -1: the gradient
+  int heads_per_block;
+};
+
+__device__ __forceinline__ unsigned long long turn_fraction(double freq) {
+  const double t = freq * 0.15915494309189533577;  // 1 / (2 pi)
+  return static_cast<unsigned long long>((t - floor(t)) * 18446744073709551616.0);
+}
+__device__ __forceinline__ long long position(const Params& p, int axis, int b, int i) {
+  long long x = p.start + (p.add_index ? i : 0);
+  if (p.pos) {
+    const long long at = axis * p.pa + b * p.pb + i * p.pn;
+    x += p.pos64 ? static_cast<const long long*>(p.pos)[at]
+                 : (long long)static_cast<const int*>(p.pos)[at];
+  }
+  return x;
+}
+__device__ __forceinline__ void turn(const Params& p, int pair, int b, int i, float& c, float& s) {
+  const int axis = p.axis ? min((int)p.axis[pair], p.axes - 1) : 0;
+  const unsigned long long a = static_cast<unsigned long long>(position(p, axis, b, i)) *
+                               turn_fraction(p.freq[pair]);
+  // upper half as a signed fraction of half a turn in [-1, 1): angle = pi * x
+  const float x = (float)(int)(a >> 32) * (1.f / 2147483648.f);
+  sincospif(x, &s, &c);
+  c *= p.scale;
+  s *= p.scale * p.sign;
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]);
+template <>
+__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+template <>
+__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  using sm100::pack_bf16x2;
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                            pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+// Heads [h0, h1) of the two tensors counted one after the other.
+// grid (ceil(tokens * units / kThreads), head blocks), block kThreads.  A token has R/16 units of
+// eight pairs and, out of place, (D - R)/16 units that copy sixteen dimensions.
+// Needs R % 16 == 0, D % 16 == 0 and 16-byte aligned rows.
+template <typename T, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const Params p) {
+  const int turning = p.R / 16, units = turning + (p.copy_tail ? (p.D - p.R) / 16 : 0);
+  const long long g = (long long)blockIdx.x * kThreads + threadIdx.x;
+  const long long token = g / units;
+  const int u = (int)(g - token * units);
+  if (token >= (long long)p.B * p.n) return;
+  const int b = (int)(token / p.n), i = (int)(token - (long long)b * p.n);
+  const bool turns = u < turning;
+  float c[kPairs], s[kPairs];
+  if (turns) {
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) turn(p, u * kPairs + k, b, i, c[k], s[k]);
+  }
+  const int d0 = turns ? (kInterleaved ? u * 16 : u * 8) : p.R + (u - turning) * 16;
+  const int d1 = turns && !kInterleaved ? d0 + p.R / 2 : d0 + 8;
+  const int h0 = blockIdx.y * p.heads_per_block;
+  const int h1 = min(h0 + p.heads_per_block, p.t[0].heads + p.t[1].heads);
+#pragma unroll 2
+  for (int hh = h0; hh < h1; ++hh) {
+    const int w = hh >= p.t[0].heads;
+    const Tensor& t = p.t[w];
+    const int h = hh - (w ? p.t[0].heads : 0);
+    const T* x = static_cast<const T*>(t.x) + b * t.xb + h * t.xh + i * t.xn;
+    T* y = static_cast<T*>(t.y) + b * t.yb + h * t.yh + i * t.yn;
+    float v0[8], v1[8], o0[8], o1[8];
+    load8<T>(x + d0, v0);
+    load8<T>(x + d1, v1);
+    if (!turns) {
+      store8(y + d0, v0);
+      store8(y + d1, v1);
+      continue;
+    }
+    if (kInterleaved) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        o0[2 * k] = v0[2 * k] * c[k] - v0[2 * k + 1] * s[k];
+        o0[2 * k + 1] = v0[2 * k + 1] * c[k] + v0[2 * k] * s[k];
+        o1[2 * k] = v1[2 * k] * c[4 + k] - v1[2 * k + 1] * s[4 + k];
+        o1[2 * k + 1] = v1[2 * k + 1] * c[4 + k] + v1[2 * k] * s[4 + k];
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        o0[k] = v0[k] * c[k] - v1[k] * s[k];
+        o1[k] = v1[k] * c[k] + v0[k] * s[k];
+      }
+    }
+    store8(y + d0, o0);
+    store8(y + d1, o1);
+  }
+}
+
+// The same for every even R, every D and strides that are not whole vectors: a thread turns one
+// pair, or copies one dimension past R, of every head.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) rotary_any_kernel(const Params p) {
+  const int turning = p.R / 2, units = turning + (p.copy_tail ? p.D - p.R : 0);
+  const long long g = (long long)blockIdx.x * kThreads + threadIdx.x;
+  const long long token = g / units;
+  const int u = (int)(g - token * units);
+  if (token >= (long long)p.B * p.n) return;
+  const int b = (int)(token / p.n), i = (int)(token - (long long)b * p.n);
+  const bool turns = u < turning;
+  float c = 0.f, s = 0.f;
+  if (turns) turn(p, u, b, i, c, s);
+  const int d0 = turns ? (p.interleaved ? 2 * u : u) : p.R + u - turning;
+  const int d1 = turns ? (p.interleaved ? 2 * u + 1 : u + p.R / 2) : d0;
+  const int h0 = blockIdx.y * p.heads_per_block;
+  const int h1 = min(h0 + p.heads_per_block, p.t[0].heads + p.t[1].heads);
+  for (int hh = h0; hh < h1; ++hh) {
+    const int w = hh >= p.t[0].heads;
+    const Tensor& t = p.t[w];
+    const int h = hh - (w ? p.t[0].heads : 0);
+    const T* x = static_cast<const T*>(t.x) + b * t.xb + h * t.xh + i * t.xn;
+    T* y = static_cast<T*>(t.y) + b * t.yb + h * t.yh + i * t.yn;
+    const float v0 = (float)x[d0], v1 = (float)x[d1];
+    if (turns) {
+      y[d0] = (T)(v0 * c - v1 * s);
+      y[d1] = (T)(v1 * c + v0 * s);
+    } else {
+      y[d0] = x[d0];
+    }
+  }
+}
+
+}  // namespace rotary
+}  // namespace rehyat

@@ -1,0 +1,413 @@
+// Host side of the sequence operators (rotary positions, decayed linear attention): argument
+// checks, the choice of segments, workspace plans and launches.  Included by rehyat.cu after its
+// helpers (fail, RH_TRY, cuda_check, Carve).
+#pragma once
+
+#include "decay.cuh"
+#include "rotary.cuh"
+
+namespace {
+
+using rehyat::decay::Pass;
+using rehyat::decay::Rows;
+
+// log_decay, lengths and states are read in place by kernels that index them from these sizes.
+int check_decay(const rehyat_decay_args& a, rehyat_dtype dt) {
+  if (dt != REHYAT_F32 && dt != REHYAT_BF16) return fail(REHYAT_ERR_DTYPE, "unknown dtype %d", (int)dt);
+  if (a.B < 1 || a.H < 1 || a.Hk < 1 || a.N < 0 || a.D < 1)
+    return fail(REHYAT_ERR_ARG, "need B, H, Hk, D >= 1 and N >= 0 (B=%d H=%d Hk=%d N=%d D=%d)", a.B,
+                a.H, a.Hk, a.N, a.D);
+  if (a.H % a.Hk) return fail(REHYAT_ERR_ARG, "Hk=%d must divide H=%d", a.Hk, a.H);
+  if (a.D % 8 || a.D > rehyat::decay::kMaxD)
+    return fail(REHYAT_ERR_SHAPE, "D=%d must be a multiple of 8 up to %d", a.D,
+                rehyat::decay::kMaxD);
+  if (a.B > 65535 || (long long)a.B * a.H > 65535)
+    return fail(REHYAT_ERR_SHAPE, "B*H = %lld exceeds 65535", (long long)a.B * a.H);
+  if (a.N > (1 << 30)) return fail(REHYAT_ERR_ARG, "sequence too long");
+  if (!std::isfinite(a.scale)) return fail(REHYAT_ERR_ARG, "scale must be finite");
+  return REHYAT_OK;
+}
+
+// A strided [B, heads, N, D] tensor: aligned, whole 16-byte strides, rows that do not overlap.
+int check_rows(const char* what, const void* p, const rehyat_strides& s, int B, int heads, int N,
+               int D, rehyat_dtype dt) {
+  const int el = dt == REHYAT_BF16 ? 2 : 4;
+  if (N == 0) return REHYAT_OK;
+  if (!p) return fail(REHYAT_ERR_ARG, "null pointer (%s)", what);
+  if (!aligned16(p)) return fail(REHYAT_ERR_ALIGN, "%s is not 16-byte aligned", what);
+  const long long st[3] = {s.batch, s.head, s.row};
+  const int size[3] = {B, heads, N};
+  for (int i = 0; i < 3; ++i) {
+    if (size[i] == 1) continue;
+    if (st[i] < D)
+      return fail(REHYAT_ERR_ARG, "%s: stride %lld of a dimension of %d is below D=%d", what, st[i],
+                  size[i], D);
+    if ((st[i] * el) % 16)
+      return fail(REHYAT_ERR_ALIGN, "%s: stride %lld is not a multiple of 16 bytes", what, st[i]);
+    if (st[i] * el >= (1LL << 40)) return fail(REHYAT_ERR_ARG, "%s: stride %lld too long", what, st[i]);
+  }
+  return REHYAT_OK;
+}
+
+Rows rows_of(const void* p, const rehyat_strides& s, int group) {
+  return Rows{p, s.batch, s.head, s.row, group};
+}
+
+// Segments of a sequence: one CTA each, so their number trades whole waves of the 148 SMs against
+// the state pass that more than one segment needs (about half the work of the row pass).  `blocks`
+// 128-row blocks; +1 block a CTA for its start.
+struct Segments {
+  int n, rows;
+};
+Segments decay_segments(int BH, int N, bool states_anyway) {
+  const int blocks = (N + rehyat::decay::kBlockRows - 1) / rehyat::decay::kBlockRows;
+  Segments best{1, blocks > 0 ? blocks * rehyat::decay::kBlockRows : rehyat::decay::kBlockRows};
+  long long best_cost = -1;
+  for (int n = 1; n <= blocks && n <= 256; ++n) {
+    const int per = (blocks + n - 1) / n;
+    const int used = (blocks + per - 1) / per;  // segments that hold rows
+    if (used != n) continue;
+    const long long waves = ((long long)BH * n + 147) / 148;
+    const long long cost = waves * (per + 1) * (n > 1 || states_anyway ? 3 : 2);
+    if (best_cost < 0 || cost < best_cost) {
+      best_cost = cost;
+      best = Segments{n, per * rehyat::decay::kBlockRows};
+    }
+  }
+  return best;
+}
+
+struct DecayPlan {
+  Segments seg;
+  size_t fwd, bwd, part, total;
+};
+DecayPlan plan_decay(const rehyat_decay_args& a, bool backward) {
+  DecayPlan p{};
+  const size_t BH = (size_t)a.B * a.H;
+  p.seg = decay_segments((int)BH, a.N, true);
+  Carve cv;
+  const size_t states = BH * p.seg.n * a.D * a.D * 4;
+  p.fwd = cv.take(states);
+  if (backward) {
+    p.bwd = cv.take(states);
+    // per query head, where dk and dv are sums over the heads that share a key/value head
+    p.part = cv.take(a.H != a.Hk ? BH * (size_t)a.N * a.D * 4 : 0);
+  }
+  p.total = cv.off;
+  return p;
+}
+
+template <typename T>
+int launch_decay_states_inst(const Pass& p, cudaStream_t st) {
+  auto k = rehyat::decay::decay_states_kernel<T>;
+  const int smem = rehyat::decay::states_smem_floats(rehyat::decay::padded(p.D)) * 4;
+  RH_TRY(cuda_check(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
+                    "decay states attr"));
+  k<<<dim3(p.nseg, p.B * p.H), rehyat::decay::kThreads, smem, st>>>(p);
+  return cuda_check(cudaGetLastError(), "decay states launch");
+}
+int launch_decay_states(const Pass& p, rehyat_dtype dt, cudaStream_t st) {
+  return dt == REHYAT_BF16 ? launch_decay_states_inst<__nv_bfloat16>(p, st)
+                           : launch_decay_states_inst<float>(p, st);
+}
+
+template <typename T, typename TOut>
+int launch_decay_rows_inst(const Pass& p, cudaStream_t st) {
+  auto k = rehyat::decay::decay_rows_kernel<T, TOut>;
+  const int smem = rehyat::decay::rows_smem_floats(rehyat::decay::padded(p.D)) * 4;
+  RH_TRY(cuda_check(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
+                    "decay rows attr"));
+  k<<<dim3(p.nseg, p.B * p.H), rehyat::decay::kThreads, smem, st>>>(p);
+  return cuda_check(cudaGetLastError(), "decay rows launch");
+}
+int launch_decay_rows(const Pass& p, rehyat_dtype dt, bool out_f32, cudaStream_t st) {
+  if (dt == REHYAT_F32) return launch_decay_rows_inst<float, float>(p, st);
+  return out_f32 ? launch_decay_rows_inst<__nv_bfloat16, float>(p, st)
+                 : launch_decay_rows_inst<__nv_bfloat16, __nv_bfloat16>(p, st);
+}
+
+int launch_decay_scan(const Pass& p, const float* S0, float* last, bool need_prefix,
+                      cudaStream_t st) {
+  const int n4 = p.D * p.D / 4;
+  rehyat::decay::decay_scan_kernel<<<dim3((n4 + 255) / 256, p.B * p.H), 256, 0, st>>>(
+      p.delta, S0, last, p.log_decay, p.lengths, p.H, p.N, p.D, p.nseg, p.seg_rows, p.reverse,
+      need_prefix);
+  return cuda_check(cudaGetLastError(), "decay scan launch");
+}
+
+// The state before every segment of a pass (rows b, c; time direction and e as in `p`) from `S0`
+// (or zero), and the state after the last into `last` unless null.  *prefix: where the row pass
+// reads it ([B*H][nseg][D][D]), null for zero.
+int decay_prefix(Pass p, rehyat_dtype dt, const float* S0, float* last, const float** prefix,
+                 cudaStream_t st) {
+  const bool many = p.nseg > 1;
+  *prefix = nullptr;
+  if (!many && !last) {
+    *prefix = S0;
+    return REHYAT_OK;
+  }
+  if (p.N > 0) {
+    p.seg_skip = last ? -1 : (p.reverse ? 0 : p.nseg - 1);
+    RH_TRY(launch_decay_states(p, dt, st));
+  }
+  // the row pass reads the workspace's copy of S0, since `last` may be S0
+  RH_TRY(launch_decay_scan(p, S0, last, many || S0, st));
+  if (many || S0) *prefix = p.delta;
+  return REHYAT_OK;
+}
+
+Pass decay_pass(const rehyat_decay_args& a, const float* log_decay, const int* lengths,
+                const Segments& s) {
+  Pass p{};
+  p.log_decay = log_decay;
+  p.lengths = lengths;
+  p.B = a.B; p.H = a.H; p.N = a.N; p.D = a.D;
+  p.nseg = s.n; p.seg_rows = s.rows;
+  p.seg_skip = -1;
+  p.sp = p.si = p.sd = 1.f;
+  return p;
+}
+
+int check_states(const char* what, const float* S) {
+  if (S && !aligned16(S)) return fail(REHYAT_ERR_ALIGN, "%s is not 16-byte aligned", what);
+  return REHYAT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int rehyat_rotary(rehyat_rotary_args a, rehyat_dtype dt, const void* q, rehyat_strides sq,
+                  const void* k, rehyat_strides sk, const double* freq, const unsigned char* axis,
+                  const void* pos, void* q_out, rehyat_strides sqo, void* k_out,
+                  rehyat_strides sko, void* stream) {
+  g_msg[0] = 0;
+  if (dt != REHYAT_F32 && dt != REHYAT_BF16) return fail(REHYAT_ERR_DTYPE, "unknown dtype %d", (int)dt);
+  if (a.B < 1 || a.n < 0 || a.Hq < 1 || a.Hk < 0 || a.D < 1)
+    return fail(REHYAT_ERR_ARG, "need B, Hq, D >= 1 and n, Hk >= 0 (B=%d n=%d Hq=%d Hk=%d D=%d)", a.B,
+                a.n, a.Hq, a.Hk, a.D);
+  if (a.R < 2 || a.R % 2 || a.R > a.D)
+    return fail(REHYAT_ERR_SHAPE, "R=%d must be even, within 2 .. D=%d", a.R, a.D);
+  if (a.axes < 1 || a.axes > rehyat::rotary::kMaxAxes)
+    return fail(REHYAT_ERR_ARG, "axes=%d outside 1 .. %d", a.axes, rehyat::rotary::kMaxAxes);
+  if (!std::isfinite(a.scale)) return fail(REHYAT_ERR_ARG, "scale must be finite");
+  if (a.n == 0) return REHYAT_OK;
+  if (!q || !q_out || !freq || (a.Hk > 0 && (!k || !k_out)))
+    return fail(REHYAT_ERR_ARG, "null pointer");
+  const bool bf16 = dt == REHYAT_BF16;
+  const int el = bf16 ? 2 : 4;
+  rehyat::rotary::Params p{};
+  p.t[0] = {q, q_out, sq.batch, sq.head, sq.row, sqo.batch, sqo.head, sqo.row, a.Hq};
+  p.t[1] = {k, k_out, sk.batch, sk.head, sk.row, sko.batch, sko.head, sko.row, a.Hk};
+  bool whole = a.R % 16 == 0 && a.D % 16 == 0, in_place = true;
+  for (int i = 0; i < (a.Hk ? 2 : 1); ++i) {
+    const rehyat::rotary::Tensor& t = p.t[i];
+    in_place &= t.x == t.y;
+    if (t.x == t.y && (t.xb != t.yb || t.xh != t.yh || t.xn != t.yn))
+      return fail(REHYAT_ERR_ARG, "in place needs the same strides in and out");
+    const long long st[6] = {t.xb, t.xh, t.xn, t.yb, t.yh, t.yn};
+    const int size[3] = {a.B, t.heads, a.n};
+    whole &= aligned16(t.x) && aligned16(t.y);
+    for (int j = 0; j < 6; ++j)
+      if (size[j % 3] > 1) whole &= (st[j] * el) % 16 == 0;
+  }
+  p.B = a.B; p.n = a.n; p.D = a.D; p.R = a.R;
+  p.interleaved = a.interleaved; p.copy_tail = !in_place && a.R < a.D;
+  p.freq = freq; p.axis = axis; p.pos = pos; p.pos64 = a.pos64; p.axes = a.axes;
+  p.pa = a.pos_axis; p.pb = a.pos_batch; p.pn = a.pos_token;
+  p.add_index = a.add_index; p.start = a.start;
+  p.scale = a.scale; p.sign = a.inverse ? -1.f : 1.f;
+  const int per = whole ? 16 : 2;  // dimensions a thread turns; it copies 16 or 1
+  const long long units = a.R / per + (p.copy_tail ? (a.D - a.R) / (whole ? 16 : 1) : 0);
+  const long long threads = (long long)a.B * a.n * units;
+  const long long blocks = (threads + rehyat::rotary::kThreads - 1) / rehyat::rotary::kThreads;
+  if (blocks > 0x7fffffffLL) return fail(REHYAT_ERR_ARG, "too many tokens");
+  // heads are dealt out over blocks until the SMs have eight blocks each: the sines and cosines
+  // are formed once per block of heads
+  const int heads = a.Hq + a.Hk;
+  long long split = (148 * 8 + blocks - 1) / blocks;
+  if (split > heads) split = heads;
+  p.heads_per_block = (int)((heads + split - 1) / split);
+  const dim3 grid((unsigned)blocks, (unsigned)((heads + p.heads_per_block - 1) / p.heads_per_block));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  using namespace rehyat::rotary;
+  if (whole) {
+    auto kern = bf16 ? (a.interleaved ? rotary_kernel<__nv_bfloat16, true>
+                                      : rotary_kernel<__nv_bfloat16, false>)
+                     : (a.interleaved ? rotary_kernel<float, true> : rotary_kernel<float, false>);
+    kern<<<grid, kThreads, 0, st>>>(p);
+  } else {
+    auto kern = bf16 ? rotary_any_kernel<__nv_bfloat16> : rotary_any_kernel<float>;
+    kern<<<grid, kThreads, 0, st>>>(p);
+  }
+  return cuda_check(cudaGetLastError(), "rotary launch");
+}
+
+int rehyat_decay_workspace_size(rehyat_decay_args a, rehyat_dtype dt, int backward,
+                                size_t* bytes) {
+  g_msg[0] = 0;
+  RH_TRY(check_decay(a, dt));
+  if (!bytes) return fail(REHYAT_ERR_ARG, "null pointer");
+  *bytes = plan_decay(a, backward != 0).total;
+  return REHYAT_OK;
+}
+
+int rehyat_decay_forward(rehyat_decay_args a, rehyat_dtype dt, const void* q, rehyat_strides sq,
+                         const void* k, rehyat_strides sk, const void* v, rehyat_strides sv,
+                         const float* log_decay, const int* lengths, const float* S0, void* out,
+                         rehyat_strides so, float* S_last, void* workspace, size_t ws_bytes,
+                         void* stream) {
+  g_msg[0] = 0;
+  RH_TRY(check_decay(a, dt));
+  if (!log_decay) return fail(REHYAT_ERR_ARG, "null pointer (log_decay)");
+  RH_TRY(check_rows("q", q, sq, a.B, a.H, a.N, a.D, dt));
+  RH_TRY(check_rows("k", k, sk, a.B, a.Hk, a.N, a.D, dt));
+  RH_TRY(check_rows("v", v, sv, a.B, a.Hk, a.N, a.D, dt));
+  RH_TRY(check_rows("out", out, so, a.B, a.H, a.N, a.D, dt));
+  RH_TRY(check_states("S0", S0));
+  RH_TRY(check_states("S_last", S_last));
+  const DecayPlan pl = plan_decay(a, false);
+  if (!workspace || ws_bytes < pl.total)
+    return fail(REHYAT_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", pl.total, ws_bytes);
+  if (!aligned16(workspace)) return fail(REHYAT_ERR_ALIGN, "workspace is not 16-byte aligned");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int group = a.H / a.Hk;
+  Pass p = decay_pass(a, log_decay, lengths, pl.seg);
+  p.a = rows_of(q, sq, 1);
+  p.b = rows_of(k, sk, group);
+  p.c = rows_of(v, sv, group);
+  p.e = 1;
+  p.sp = p.si = a.scale;
+  p.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.fwd);
+  RH_TRY(decay_prefix(p, dt, S0, S_last, &p.prefix, st));
+  if (a.N == 0) return REHYAT_OK;
+  p.out = out;
+  p.ob = so.batch; p.oh = so.head; p.on = so.row;
+  return launch_decay_rows(p, dt, false, st);
+}
+
+int rehyat_decay_backward(rehyat_decay_args a, rehyat_dtype dt, const void* q, rehyat_strides sq,
+                          const void* k, rehyat_strides sk, const void* v, rehyat_strides sv,
+                          const float* log_decay, const int* lengths, const float* S0,
+                          const void* dout, rehyat_strides sdo, const float* dS_last, void* dq,
+                          rehyat_strides sdq, void* dk, rehyat_strides sdk, void* dv,
+                          rehyat_strides sdv, float* dS0, void* workspace, size_t ws_bytes,
+                          void* stream) {
+  g_msg[0] = 0;
+  RH_TRY(check_decay(a, dt));
+  if (!log_decay) return fail(REHYAT_ERR_ARG, "null pointer (log_decay)");
+  RH_TRY(check_rows("q", q, sq, a.B, a.H, a.N, a.D, dt));
+  RH_TRY(check_rows("k", k, sk, a.B, a.Hk, a.N, a.D, dt));
+  RH_TRY(check_rows("v", v, sv, a.B, a.Hk, a.N, a.D, dt));
+  RH_TRY(check_rows("dout", dout, sdo, a.B, a.H, a.N, a.D, dt));
+  RH_TRY(check_rows("dq", dq, sdq, a.B, a.H, a.N, a.D, dt));
+  RH_TRY(check_rows("dk", dk, sdk, a.B, a.Hk, a.N, a.D, dt));
+  RH_TRY(check_rows("dv", dv, sdv, a.B, a.Hk, a.N, a.D, dt));
+  RH_TRY(check_states("S0", S0));
+  RH_TRY(check_states("dS_last", dS_last));
+  RH_TRY(check_states("dS0", dS0));
+  const DecayPlan pl = plan_decay(a, true);
+  if (!workspace || ws_bytes < pl.total)
+    return fail(REHYAT_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", pl.total, ws_bytes);
+  if (!aligned16(workspace)) return fail(REHYAT_ERR_ALIGN, "workspace is not 16-byte aligned");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const int group = a.H / a.Hk;
+  const Rows rq = rows_of(q, sq, 1), rk = rows_of(k, sk, group), rv = rows_of(v, sv, group),
+             rdo = rows_of(dout, sdo, 1);
+
+  // dQ: forward in time over the states of the prompt, transposed
+  Pass f = decay_pass(a, log_decay, lengths, pl.seg);
+  f.delta = reinterpret_cast<float*>(ws + pl.fwd);
+  f.e = 1;
+  if (a.N > 0) {
+    f.b = rk;
+    f.c = rv;
+    RH_TRY(decay_prefix(f, dt, S0, nullptr, &f.prefix, st));
+    f.a = rdo;
+    f.b = rv;
+    f.c = rk;
+    f.transposed = 1;
+    f.sp = f.si = a.scale;
+    f.out = dq;
+    f.ob = sdq.batch; f.oh = sdq.head; f.on = sdq.row;
+    RH_TRY(launch_decay_rows(f, dt, false, st));
+  }
+
+  // dK, dV: backward in time over the gradient of the state, sum of scale * q dO^T
+  Pass r = decay_pass(a, log_decay, lengths, pl.seg);
+  r.delta = reinterpret_cast<float*>(ws + pl.bwd);
+  r.reverse = 1;
+  r.e = 0;
+  r.b = rq;
+  r.c = rdo;
+  r.sp = r.sd = a.scale;
+  RH_TRY(decay_prefix(r, dt, dS_last, dS0, &r.prefix, st));
+  if (a.N == 0) return REHYAT_OK;
+  float* part = reinterpret_cast<float*>(ws + pl.part);
+  for (int i = 0; i < 2; ++i) {
+    Pass p = r;
+    p.a = i ? rk : rv;
+    p.b = i ? rq : rdo;
+    p.c = i ? rdo : rq;
+    p.transposed = i ? 0 : 1;
+    void* dst = i ? dv : dk;
+    const rehyat_strides& s = i ? sdv : sdk;
+    if (group == 1) {
+      p.out = dst;
+      p.ob = s.batch; p.oh = s.head; p.on = s.row;
+      RH_TRY(launch_decay_rows(p, dt, false, st));
+      continue;
+    }
+    p.out = part;
+    p.on = a.D; p.oh = (long long)a.N * a.D; p.ob = p.oh * a.H;
+    RH_TRY(launch_decay_rows(p, dt, true, st));
+    const long long vec = (long long)a.N * a.D / 4;
+    const dim3 grid((unsigned)(vec / 1024 + 1 < 4096 ? vec / 1024 + 1 : 4096), a.B * a.Hk);
+    if (dt == REHYAT_BF16)
+      rehyat::decay::decay_group_sum_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(
+          part, static_cast<__nv_bfloat16*>(dst), s.batch, s.head, s.row, a.Hk, group, a.N, a.D);
+    else
+      rehyat::decay::decay_group_sum_kernel<float><<<grid, 256, 0, st>>>(
+          part, static_cast<float*>(dst), s.batch, s.head, s.row, a.Hk, group, a.N, a.D);
+    RH_TRY(cuda_check(cudaGetLastError(), "decay group sum launch"));
+  }
+  return REHYAT_OK;
+}
+
+int rehyat_decay_step(rehyat_decay_args a, rehyat_dtype dt, const void* q, rehyat_strides sq,
+                      const void* k, rehyat_strides sk, const void* v, rehyat_strides sv,
+                      const float* log_decay, float* state, int pool, const int* slots, void* out,
+                      rehyat_strides so, void* stream) {
+  g_msg[0] = 0;
+  a.N = 1;
+  RH_TRY(check_decay(a, dt));
+  if (!log_decay || !state) return fail(REHYAT_ERR_ARG, "null pointer");
+  RH_TRY(check_rows("q", q, sq, a.B, a.H, 1, a.D, dt));
+  RH_TRY(check_rows("k", k, sk, a.B, a.Hk, 1, a.D, dt));
+  RH_TRY(check_rows("v", v, sv, a.B, a.Hk, 1, a.D, dt));
+  RH_TRY(check_rows("out", out, so, a.B, a.H, 1, a.D, dt));
+  RH_TRY(check_states("state", state));
+  if (pool < 1 || (!slots && pool < a.B))
+    return fail(REHYAT_ERR_ARG, "a pool of %d states for %d sequences", pool, a.B);
+  rehyat::decay::StepParams p{};
+  const int group = a.H / a.Hk;
+  p.q = rows_of(q, sq, 1);
+  p.k = rows_of(k, sk, group);
+  p.v = rows_of(v, sv, group);
+  p.out = out;
+  p.ob = so.batch; p.oh = so.head;
+  p.log_decay = log_decay; p.state = state; p.slots = slots;
+  p.B = a.B; p.H = a.H; p.D = a.D; p.pool = pool; p.scale = a.scale;
+  using namespace rehyat::decay;
+  const dim3 grid((a.D + kStepCols - 1) / kStepCols, a.H, a.B);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int passes = (a.D + 15) / 16;  // of 16 rows
+  const bool bf16 = dt == REHYAT_BF16;
+  auto kern = passes <= 4 ? (bf16 ? decay_step_kernel<__nv_bfloat16, 4> : decay_step_kernel<float, 4>)
+                          : (bf16 ? decay_step_kernel<__nv_bfloat16, 8> : decay_step_kernel<float, 8>);
+  kern<<<grid, kStepThreads, 0, st>>>(p);
+  return cuda_check(cudaGetLastError(), "decay step launch");
+}
+
+}  // extern "C"
