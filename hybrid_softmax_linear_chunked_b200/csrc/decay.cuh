@@ -1,6 +1,6 @@
 // Linear attention with a decay L = exp(log_decay[h]) per head, CUDA-core kernels: fp32 prompts and
-// gradients, the scan that joins segments (fp32 and bf16), the single-token step, and the sum over
-// query heads that share a key/value head.
+// gradients (the bf16 ones are in decay_bf16.cuh), the scan that joins segments, the single-token
+// step, and the sum over query heads that share a key/value head.
 //
 // One form serves the prompt and its gradients.  A pass reads rows a, b, c and writes
 //     out_i = sp * sum_{j in past(i)} L^|i-j| (a_i . b_j) c_j  +  si * L^(t_i + e) a_i^T S ,
@@ -98,15 +98,14 @@ __device__ __forceinline__ float4 mul4(float s, float4 v) {
 
 // Rows [r0, r0 + kC) of one head into shared memory as fp32 [kC][ld], columns [D, Dp) and rows at
 // or past `end` as zeros whatever the tensor holds there.
-template <typename T>
 __device__ __forceinline__ void load_rows(float* dst, int ld, const Rows& t, int b, int h, int r0,
                                           int end, int D, int Dp) {
-  const T* src = static_cast<const T*>(t.p) + b * t.sb + (h / t.group) * t.sh;
+  const float* src = static_cast<const float*>(t.p) + b * t.sb + (h / t.group) * t.sh;
   const int v4 = Dp / 4;
   for (int i = threadIdx.x; i < kC * v4; i += kThreads) {
     const int r = i / v4, c = (i - r * v4) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r0 + r < end && c < D) x = load4<T>(src + (long long)(r0 + r) * t.sn + c);
+    if (r0 + r < end && c < D) x = load4<float>(src + (long long)(r0 + r) * t.sn + c);
     *reinterpret_cast<float4*>(dst + r * ld + c) = x;
   }
 }
@@ -161,7 +160,6 @@ __device__ __forceinline__ int outer_row(const Outer& o, int i) {
 
 // Each segment's own sum: delta = sd * sum_j L^(n - t_j - e) b_j c_j^T over its n valid rows.
 // grid (nseg, B*H), block 256.
-template <typename T>
 __global__ void __launch_bounds__(kThreads, 1) decay_states_kernel(const Pass p) {
   extern __shared__ __align__(16) float smf[];
   const int seg = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh - b * p.H;
@@ -178,8 +176,8 @@ __global__ void __launch_bounds__(kThreads, 1) decay_states_kernel(const Pass p)
   for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int r0 = r_begin; r0 < r_end; r0 += kC) {
     __syncthreads();
-    load_rows<T>(sb, ld, p.b, b, h, r0, r_end, p.D, Dp);
-    load_rows<T>(sc, ld, p.c, b, h, r0, r_end, p.D, Dp);
+    load_rows(sb, ld, p.b, b, h, r0, r_end, p.D, Dp);
+    load_rows(sc, ld, p.c, b, h, r0, r_end, p.D, Dp);
     __syncthreads();
     const int rows = min(kC, r_end - r0);
     if (o.on) {
@@ -236,7 +234,6 @@ __global__ void __launch_bounds__(256)
 // The rows of one segment: chunks of kC in time order, the state [D][D] carried in shared memory.
 // Bound by the fp32 pipes: 2 kC D (kC + 2 D) multiply-adds a chunk.
 // grid (nseg, B*H), block 256.
-template <typename T, typename TOut>
 __global__ void __launch_bounds__(kThreads, 1) decay_rows_kernel(const Pass p) {
   extern __shared__ __align__(16) float smf[];
   const int seg = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh - b * p.H;
@@ -251,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_rows_kernel(const Pass p) {
   const int n = length_of(p.lengths, b, p.N);
   const int r_begin = seg * p.seg_rows, r_stop = min(r_begin + p.seg_rows, p.N);
   const int r_end = min(r_stop, n);
-  TOut* out = static_cast<TOut*>(p.out) + b * p.ob + h * p.oh;
+  float* out = static_cast<float*>(p.out) + b * p.ob + h * p.oh;
 
   for (int i = tid; i < Dp * (Dp / 4); i += kThreads) {
     const int r = i / (Dp / 4), c = (i - r * (Dp / 4)) * 4;
@@ -285,9 +282,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_rows_kernel(const Pass p) {
       }
       continue;
     }
-    load_rows<T>(sa, ld, p.a, b, h, r0, r_end, p.D, Dp);
-    load_rows<T>(sb, ld, p.b, b, h, r0, r_end, p.D, Dp);
-    load_rows<T>(sc, ld, p.c, b, h, r0, r_end, p.D, Dp);
+    load_rows(sa, ld, p.a, b, h, r0, r_end, p.D, Dp);
+    load_rows(sb, ld, p.b, b, h, r0, r_end, p.D, Dp);
+    load_rows(sc, ld, p.c, b, h, r0, r_end, p.D, Dp);
     __syncthreads();
     {  // P = sp * L^|i-j| (a_i . b_j) over the past of i, 4 x 4 a thread (columns 16 apart)
       const int i0 = (tid / 16) * 4, j0 = tid % 16;
@@ -365,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_rows_kernel(const Pass p) {
         const int r = orow + u;
         if (r0 + r >= r_stop) continue;
         if (r >= rows) acc[u][0] = acc[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-        TOut* dst = out + (long long)(r0 + r) * p.on;
+        float* dst = out + (long long)(r0 + r) * p.on;
         if (ocol < p.D) store4(dst + ocol, acc[u][0]);
         if (ocol + ohalf < p.D) store4(dst + ocol + ohalf, acc[u][1]);
       }

@@ -1,0 +1,592 @@
+// Linear attention with a decay per head on the tensor cores (bf16, D <= 128): the two passes of
+// decay.cuh over 128-row chunks.
+//
+// Bound by memory once the products run on tcgen05: a chunk of the row pass moves 128 KB (a, b, c
+// in, out) for four 128^3 products, 2,048 clk of a tensor pipe against about 5,600 clk of one SM's
+// share of HBM.  So the kernels aim at keeping loads in flight: one CTA per SM, two (rows) or three
+// (states) stages of whole chunks, and one warp for each thing that waits.
+//
+// Rounded to bf16: the weighted scores P, the weighted rows b of the carried state, the state the
+// rows read, and the output; sums, states and powers are fp32.  The states pass multiplies each
+// weighted row in two bf16 parts (16 mantissa bits), so the states between segments and the last
+// state are fp32 sums of terms good to 2^-16.
+//
+// Narrow heads (D < 128) run on the same tiles: columns at and past D load as zeros (the tensor map
+// ends there) and are not stored, and the products' depth and width stop at D rounded up to 16.
+#pragma once
+
+#include "decay.cuh"
+#include "sm100.cuh"
+
+namespace rehyat {
+namespace decay {
+namespace tc {
+
+using namespace sm100;
+
+constexpr int kRows = 128;  // rows of a chunk
+constexpr uint32_t kTile = kRows * 128 * 2;
+
+__device__ __forceinline__ uint64_t kmajor_desc(uint32_t tile, int kk) {
+  return sdesc_sw128(tile + (kk >> 2) * (kRows * 128) + (kk & 3) * 32, 16, 1024);
+}
+__device__ __forceinline__ uint64_t mnmajor_desc(uint32_t tile, int kk) {
+  return sdesc_sw128(tile + kk * 16 * 128, kRows * 128, 1024);
+}
+__device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+__device__ __forceinline__ void load_tile(int site, uint8_t* dst, const CUtensorMap* m,
+                                          uint64_t* bar, int row, int h, int b, const Pass& p,
+                                          int heads) {
+  tma_load_4d_chk(site, dst, m, bar, 0, row, h, b, p.N, heads, p.B);
+  tma_load_4d_chk(site, dst + kRows * 128, m, bar, 64, row, h, b, p.N, heads, p.B);
+}
+// Eight bf16 values times w, rounded to bf16; with kTwo the rounding's remainder in a second part.
+template <bool kTwo>
+__device__ __forceinline__ uint4 scale8(uint4 x, float w, uint4& lo) {
+  uint32_t in[4] = {x.x, x.y, x.z, x.w}, hi[4], rest[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&in[i]));
+    const float a = f.x * w, b = f.y * w;
+    hi[i] = pack_bf16x2(a, b);
+    if (kTwo) {
+      const float2 h = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&hi[i]));
+      rest[i] = pack_bf16x2(a - h.x, b - h.y);
+    }
+  }
+  if (kTwo) lo = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+  return make_uint4(hi[0], hi[1], hi[2], hi[3]);
+}
+
+// ---------------------------------------------------------------------------------------------
+// States: delta = sd * sum_j L^(n - t_j - e) b_j c_j^T over a segment.
+// ---------------------------------------------------------------------------------------------
+constexpr int kStStages = 3;
+constexpr int kStMath = 256;                 // warps 0-7: weigh b, split it in two parts
+constexpr int kStThreads = kStMath + 64;     // warp 8: copies, warp 9: products
+constexpr uint32_t kStOffLo = kStStages * 2 * kTile;
+constexpr uint32_t kStSmem = kStOffLo + kTile + 1024;
+static_assert(kStSmem + 256 <= 232448, "shared memory over the limit");
+
+// Every weight is taken to the segment's end, so all chunks add into one accumulator and nothing is
+// rescaled.  grid (nseg, B*H), block 320.
+__global__ void __launch_bounds__(kStThreads, 1)
+    decay_states_bf16_kernel(const __grid_constant__ CUtensorMap tmB,
+                             const __grid_constant__ CUtensorMap tmC, const Pass p) {
+  enum { kFull = 0, kEmpty = kFull + kStStages, kReady = kEmpty + kStStages, kLoFree, kDone, kNum };
+  grid_dep_signal();
+  const int seg = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh - b * p.H;
+  if (seg == p.seg_skip) return;
+  const int r_begin = seg * p.seg_rows;
+  const int r_end = min(r_begin + p.seg_rows, length_of(p.lengths, b, p.N));
+  const int nc = (r_end - r_begin + kRows - 1) / kRows;
+  if (nc <= 0) return;  // the scan does not read the sum of no rows
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = align1024(smem_raw);
+  __shared__ __align__(8) uint64_t bars[kNum];
+  __shared__ uint32_t tmem_sh;
+  __shared__ int abort_sh;
+  volatile int* abort_flag = &abort_sh;
+  if (warp == 8) {
+    tmem_alloc(&tmem_sh, 128);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kNum; ++i) mbar_init(&bars[i], i == kReady ? kStMath : 1);
+    abort_sh = 0;
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_sh;
+  auto wait = [&](int bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(&bars[bar], parity, abort_flag));
+  };
+
+  if (warp == 8) {  // ---- copies ----
+    const int hb = h / p.b.group, hc = h / p.c.group;
+    bool ok = true;
+    int issued = 0;
+    for (int i = 0; i < nc; ++i) {
+      const int s = i % kStStages;
+      if (i >= kStStages) ok = wait(kEmpty + s, (i / kStStages - 1) & 1);
+      if (!ok) break;
+      if (lane == 0) {
+        uint8_t* dst = sm + s * 2 * kTile;
+        mbar_arrive_expect_tx(&bars[kFull + s], 2 * kTile);
+        load_tile(51, dst, &tmB, &bars[kFull + s], r_begin + i * kRows, hb, b, p, p.H / p.b.group);
+        load_tile(52, dst + kTile, &tmC, &bars[kFull + s], r_begin + i * kRows, hc, b, p,
+                  p.H / p.c.group);
+      }
+      __syncwarp();
+      ++issued;
+    }
+    if (!ok)
+      for (int i = max(0, issued - kStStages); i < issued; ++i)
+        mbar_wait_drain(&bars[kFull + i % kStStages], (i / kStStages) & 1);
+    __syncwarp();
+  } else if (warp == 9) {  // ---- products: b^T c, high and low part of b ----
+    const int w = (p.D + 15) / 16 * 16;
+    const uint32_t id = idesc_bf16(128, w, true, true);
+    const uint32_t lo = smem_u32(sm + kStOffLo);
+    bool ok = true;
+    for (int i = 0; i < nc && ok; ++i) {
+      const int s = i % kStStages;
+      ok = wait(kReady, i & 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t hi = smem_u32(sm + s * 2 * kTile), c = hi + kTile;
+        for (int kk = 0; kk < kRows / 16; ++kk) {
+          mma_ss(tmem, mnmajor_desc(hi, kk), mnmajor_desc(c, kk), id, (i > 0 || kk > 0) ? 1u : 0u);
+          mma_ss(tmem, mnmajor_desc(lo, kk), mnmajor_desc(c, kk), id, 1u);
+        }
+        mma_commit(&bars[kLoFree]);
+        mma_commit(&bars[kEmpty + s]);
+      }
+      __syncwarp();
+    }
+    if (lane == 0) mma_commit(&bars[kDone]);
+    __syncwarp();
+    mbar_wait_drain(&bars[kDone], 0);
+    __syncwarp();
+  } else {  // ---- weights: row r, columns half by half ----
+    const int r = tid & 127, half = tid >> 7;
+    const float g2 = log2_decay(p.log_decay, h);
+    bool ok = true;
+    for (int i = 0; i < nc; ++i) {
+      const int s = i % kStStages;
+      ok = wait(kFull + s, (i / kStStages) & 1);
+      if (ok && i > 0) ok = wait(kLoFree, (i - 1) & 1);
+      if (!ok) break;
+      const int row = r_begin + i * kRows + r;
+      const bool valid = row < r_end;
+      const int m = p.reverse ? row - r_begin + 1 - p.e : r_end - p.e - row;
+      const float w = valid ? p.sd * exp2f(g2 * (float)m) : 0.f;
+      uint8_t* hi = sm + s * 2 * kTile;
+      uint8_t* lo = sm + kStOffLo;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t off = sw128_offset(r, half * 64 + j * 8, kRows);
+        uint4 x = *reinterpret_cast<uint4*>(hi + off), rest;
+        if (!valid) x = make_uint4(0, 0, 0, 0);  // padding may hold anything
+        x = scale8<true>(x, w, rest);
+        *reinterpret_cast<uint4*>(hi + off) = x;
+        *reinterpret_cast<uint4*>(lo + off) = rest;
+        if (!valid) *reinterpret_cast<uint4*>(hi + kTile + off) = make_uint4(0, 0, 0, 0);
+      }
+      fence_async_smem();
+      mbar_arrive(&bars[kReady]);
+    }
+    if (ok) ok = wait(kDone, 0);
+    if (ok) {
+      tc_fence_after();
+      float* dst = p.delta + (((size_t)bh * p.nseg + seg) * p.D + r) * p.D;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int c0 = half * 64 + q * 32;
+        if (c0 >= p.D) break;
+        uint32_t v[32];
+        tmem_ld32(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0, v);
+        if (r < p.D) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (c0 + j * 4 < p.D)
+              *reinterpret_cast<float4*>(dst + c0 + j * 4) =
+                  make_float4(__uint_as_float(v[j * 4]), __uint_as_float(v[j * 4 + 1]),
+                              __uint_as_float(v[j * 4 + 2]), __uint_as_float(v[j * 4 + 3]));
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 128);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Rows.
+// ---------------------------------------------------------------------------------------------
+// warps 0-3: scores and outputs, 4-7: weights and the state, 8: copies in, 9: products, 10: copies out
+constexpr int kRwThreads = 352;
+constexpr uint32_t kRwStage = 3 * kTile;
+constexpr uint32_t kRwOffS = 2 * kRwStage;
+constexpr uint32_t kRwSmem = kRwOffS + kTile + 1024;
+static_assert(kRwSmem + 512 <= 232448, "shared memory over the limit");
+// TMEM columns: scores a b^T (P over them), P c, a S, the chunk's own b^T c
+constexpr uint32_t kColP = 0, kColIn = 128, kColSt = 256, kColAdd = 384;
+
+// A chunk i, chunk after chunk in time order:
+//   scores = a b^T -> P = sp L^|i-j| scores on the past, bf16, into TMEM     (warps 0-3)
+//   b weighted in place (after the scores have read it)                       (warps 4-7)
+//   add = b^T c;  in = P c;  st = a S                                         (warp 9)
+//   out = in + si L^(t+e) st -> over a's tile -> global                       (warps 0-3, 10)
+//   S = L^rows S + add, in registers (a row a thread), bf16 copy for a S      (warps 4-7)
+// grid (nseg, B*H), block 352.
+template <bool kReverse, bool kOutF32>
+__global__ void __launch_bounds__(kRwThreads, 1)
+    decay_rows_bf16_kernel(const __grid_constant__ CUtensorMap tmA,
+                           const __grid_constant__ CUtensorMap tmB,
+                           const __grid_constant__ CUtensorMap tmC,
+                           const __grid_constant__ CUtensorMap tmOut, const Pass p) {
+  enum {
+    kAFull = 0, kBFull = 2, kCFull = 4, kAEmpty = 6, kBEmpty = 8, kCEmpty = 10, kScores = 12,
+    kPReady, kBReady, kOFull, kOFree, kAddFull, kSReady, kStaged, kDone, kNum
+  };
+  const int seg = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh - b * p.H;
+  const int r_begin = seg * p.seg_rows, r_stop = min(r_begin + p.seg_rows, p.N);
+  const int r_end = min(r_stop, length_of(p.lengths, b, p.N));
+  const int nc = max(0, (r_end - r_begin + kRows - 1) / kRows);  // chunks that hold valid rows
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // rows of whole chunks of padding
+  {
+    const int z0 = r_begin + nc * kRows, vec = p.D * (kOutF32 ? 4 : 2) / 16;
+    uint8_t* out = static_cast<uint8_t*>(p.out);
+    for (long long i = tid; i < (long long)max(0, r_stop - z0) * vec; i += kRwThreads) {
+      const int r = z0 + (int)(i / vec), v = (int)(i % vec);
+      const long long el = b * p.ob + h * p.oh + r * p.on;
+      *reinterpret_cast<uint4*>(out + el * (kOutF32 ? 4 : 2) + v * 16) = make_uint4(0, 0, 0, 0);
+    }
+  }
+  if (nc == 0) {
+    grid_dep_wait();
+    return;
+  }
+  auto chunk_row = [&](int i) { return r_begin + (kReverse ? nc - 1 - i : i) * kRows; };
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = align1024(smem_raw);
+  __shared__ __align__(8) uint64_t bars[kNum];
+  __shared__ uint32_t tmem_sh;
+  __shared__ int abort_sh;
+  volatile int* abort_flag = &abort_sh;
+  if (warp == 8) {
+    tmem_alloc(&tmem_sh, 512);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kNum; ++i) {
+      const bool many = i == kPReady || i == kBReady || i == kOFree || i == kSReady || i == kStaged;
+      mbar_init(&bars[i], many ? 128 : 1);
+    }
+    abort_sh = 0;
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_sh;
+  const bool carried = p.prefix != nullptr;  // chunk 0 has a state to read
+  auto wait = [&](int bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(&bars[bar], parity, abort_flag));
+  };
+
+  if (warp == 8) {  // ---- copies in ----
+    const int hb = h / p.b.group, hc = h / p.c.group, ha = h / p.a.group;
+    if (lane == 0) {
+      tma_prefetch_desc(&tmA);
+      tma_prefetch_desc(&tmB);
+      tma_prefetch_desc(&tmC);
+    }
+    __syncwarp();
+    bool ok = true;
+    int n_a = 0, n_b = 0, n_c = 0;
+    auto load = [&](int i, int full, int empty, int slot, const CUtensorMap* m, int head, int heads,
+                    int& n) {
+      const int s = i & 1;
+      if (i >= 2) ok = wait(empty + s, ((i >> 1) - 1) & 1);
+      if (!ok) return;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bars[full + s], kTile);
+        load_tile(53 + slot, sm + s * kRwStage + slot * kTile, m, &bars[full + s], chunk_row(i), head,
+                  b, p, heads);
+      }
+      __syncwarp();
+      ++n;
+    };
+    for (int i = 0; i < nc && ok; ++i) {
+      load(i, kBFull, kBEmpty, 1, &tmB, hb, p.H / p.b.group, n_b);
+      if (ok) load(i, kAFull, kAEmpty, 0, &tmA, ha, p.H / p.a.group, n_a);
+      if (ok) load(i, kCFull, kCEmpty, 2, &tmC, hc, p.H / p.c.group, n_c);
+    }
+    if (!ok) {
+      auto drain = [&](int full, int n) {
+        for (int i = max(0, n - 2); i < n; ++i) mbar_wait_drain(&bars[full + (i & 1)], (i >> 1) & 1);
+      };
+      drain(kAFull, n_a);
+      drain(kBFull, n_b);
+      drain(kCFull, n_c);
+    }
+    __syncwarp();
+  } else if (warp == 9) {  // ---- products ----
+    const int kd = (p.D + 15) / 16, w = kd * 16;
+    const uint32_t id_p = idesc_bf16(128, 128, false, false);  // a (K-major) x b (K-major)
+    const uint32_t id_o = idesc_bf16(128, w, false, true);     // P or a x c or S (N-major)
+    const uint32_t id_s = idesc_bf16(128, w, true, true);      // b^T x c
+    const uint32_t sS = smem_u32(sm + kRwOffS);
+    auto tile = [&](int i, int slot) { return smem_u32(sm + (i & 1) * kRwStage + slot * kTile); };
+    auto scores = [&](int i) {
+      bool ok = wait(kAFull + (i & 1), (i >> 1) & 1) && wait(kBFull + (i & 1), (i >> 1) & 1);
+      if (!ok) return false;
+      tc_fence_after();
+      if (lane == 0) {
+        for (int kk = 0; kk < kd; ++kk)
+          mma_ss(tmem + kColP, kmajor_desc(tile(i, 0), kk), kmajor_desc(tile(i, 1), kk), id_p,
+                 kk > 0 ? 1u : 0u);
+        mma_commit(&bars[kScores]);
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = scores(0);
+    for (int i = 0; i < nc && ok; ++i) {
+      const int s = i & 1;
+      const bool last = i + 1 == nc, reads_state = i > 0 || carried;
+      // kBReady follows the arrival of chunk i - 1's sum in registers: its columns are free
+      ok = wait(kCFull + s, (i >> 1) & 1) && wait(kBReady, i & 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (lane == 0) {
+        if (!last) {
+          for (int kk = 0; kk < kRows / 16; ++kk)
+            mma_ss(tmem + kColAdd, mnmajor_desc(tile(i, 1), kk), mnmajor_desc(tile(i, 2), kk), id_s,
+                   kk > 0 ? 1u : 0u);
+          mma_commit(&bars[kAddFull]);
+        }
+        mma_commit(&bars[kBEmpty + s]);
+      }
+      __syncwarp();
+      ok = wait(kPReady, i & 1) && wait(kSReady, i & 1);
+      if (ok && i > 0) ok = wait(kOFree, (i - 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (lane == 0) {
+        for (int kk = 0; kk < kRows / 16; ++kk)
+          mma_ts(tmem + kColIn, tmem + kColP + kk * 8, mnmajor_desc(tile(i, 2), kk), id_o,
+                 kk > 0 ? 1u : 0u);
+        mma_commit(&bars[kCEmpty + s]);
+        if (reads_state)
+          for (int kk = 0; kk < kd; ++kk)
+            mma_ss(tmem + kColSt, kmajor_desc(tile(i, 0), kk), mnmajor_desc(sS, kk), id_o,
+                   kk > 0 ? 1u : 0u);
+        mma_commit(&bars[kOFull]);
+      }
+      __syncwarp();
+      if (!last) ok = scores(i + 1);
+    }
+    if (lane == 0) mma_commit(&bars[kDone]);
+    __syncwarp();
+    mbar_wait_drain(&bars[kDone], 0);
+    __syncwarp();
+  } else if (warp == 10) {  // ---- copies out; a's tile is free once its output has left ----
+    bool ok = true;
+    for (int i = 0; i < nc && ok; ++i) {
+      ok = wait(kStaged, i & 1);
+      if (!ok) break;
+      if (lane == 0) {
+        if (!kOutF32) {
+          const uint8_t* src = sm + (i & 1) * kRwStage;
+          tma_store_4d_chk(56, &tmOut, src, 0, chunk_row(i), h, b, p.N, p.H, p.B);
+          if (p.D > 64)
+            tma_store_4d_chk(56, &tmOut, src + kRows * 128, 64, chunk_row(i), h, b, p.N, p.H, p.B);
+          bulk_commit_group();
+          bulk_wait_read_all();
+        }
+        mbar_arrive(&bars[kAEmpty + (i & 1)]);
+      }
+      __syncwarp();
+    }
+    if (!kOutF32 && lane == 0) bulk_wait_all();
+    __syncwarp();
+  } else if (warp < 4) {  // ---- scores and outputs: row r of the chunk = TMEM lane ----
+    const int r = tid;
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const float g2 = log2_decay(p.log_decay, h);
+    // L^|i-j| off the diagonal 32 x 32 blocks = (power of the row to the block's near edge) x
+    // (power within the block), both exponents >= 0; on the diagonal one power an element
+    float in_block[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) in_block[j] = ex2(g2 * (float)(kReverse ? j : 31 - j));
+    bool ok = true;
+    for (int i = 0; i < nc; ++i) {
+      const int row0 = chunk_row(i), rows = min(kRows, r_end - row0);
+      ok = wait(kScores, i & 1);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int jb = 0; jb < 4; ++jb) {
+        uint32_t pk[16];
+        if (kReverse ? jb < warp : jb > warp) {  // no past here
+#pragma unroll
+          for (int j = 0; j < 16; ++j) pk[j] = 0u;
+        } else {
+          uint32_t v[32];
+          tmem_ld32(tmem + lanes + kColP + jb * 32, v);
+          float f[32];
+          if (jb == warp || (kReverse && rows < kRows)) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int c = jb * 32 + j, d = kReverse ? c - r : r - c;
+              const bool past = d >= 0 && c < rows;
+              f[j] = past ? p.sp * ex2(g2 * (float)d) * __uint_as_float(v[j]) : 0.f;
+            }
+          } else {
+            const int d = kReverse ? jb * 32 - r : r - jb * 32 - 31;
+            const float edge = p.sp * ex2(g2 * (float)d);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) f[j] = edge * in_block[j] * __uint_as_float(v[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
+        }
+        tmem_st16(tmem + lanes + kColP + jb * 16, pk);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&bars[kPReady]);
+
+      const bool reads_state = i > 0 || carried;
+      const int t = kReverse ? rows - 1 - r : r;
+      const bool valid = r < rows;
+      const float f = p.si * ex2(g2 * (float)(max(t, 0) + p.e));
+      ok = wait(kOFull, i & 1);
+      if (!ok) break;
+      tc_fence_after();
+      uint8_t* stage = sm + (i & 1) * kRwStage;
+      float* of = kOutF32 ? static_cast<float*>(p.out) + b * p.ob + h * p.oh + (row0 + r) * p.on
+                          : nullptr;
+      const int blocks = (p.D + 31) / 32;
+#pragma unroll 1
+      for (int cb = 0; cb < blocks; ++cb) {
+        uint32_t v[32];
+        float o[32];
+        tmem_ld32(tmem + lanes + kColIn + cb * 32, v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(v[j]);
+        if (reads_state) {
+          tmem_ld32(tmem + lanes + kColSt + cb * 32, v);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = fmaf(f, __uint_as_float(v[j]), o[j]);
+        }
+        if (!valid)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = 0.f;
+        if (kOutF32) {
+          if (row0 + r < r_stop)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (cb * 32 + j * 4 < p.D)
+                *reinterpret_cast<float4*>(of + cb * 32 + j * 4) =
+                    make_float4(o[j * 4], o[j * 4 + 1], o[j * 4 + 2], o[j * 4 + 3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(stage + sw128_offset(r, cb * 32 + j * 8, kRows)) =
+                make_uint4(pack_bf16x2(o[j * 8], o[j * 8 + 1]), pack_bf16x2(o[j * 8 + 2], o[j * 8 + 3]),
+                           pack_bf16x2(o[j * 8 + 4], o[j * 8 + 5]),
+                           pack_bf16x2(o[j * 8 + 6], o[j * 8 + 7]));
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&bars[kOFree]);
+      fence_async_smem();
+      mbar_arrive(&bars[kStaged]);
+    }
+  } else {  // ---- weights and the state: row r of b's tile, and row r of S = TMEM lane ----
+    const int r = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const float g2 = log2_decay(p.log_decay, h);
+    uint8_t* sS = sm + kRwOffS;
+    float S[128];
+#pragma unroll
+    for (int j = 0; j < 128; ++j) S[j] = 0.f;
+    auto publish = [&]() {  // bf16 copy of S for the next chunk's a S
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        *reinterpret_cast<uint4*>(sS + sw128_offset(r, j * 8, kRows)) = make_uint4(
+            pack_bf16x2(S[j * 8], S[j * 8 + 1]), pack_bf16x2(S[j * 8 + 2], S[j * 8 + 3]),
+            pack_bf16x2(S[j * 8 + 4], S[j * 8 + 5]), pack_bf16x2(S[j * 8 + 6], S[j * 8 + 7]));
+      fence_async_smem();
+      mbar_arrive(&bars[kSReady]);
+    };
+    grid_dep_wait();  // the prefix comes from the launch before
+    if (carried && r < p.D) {
+      const float* src = p.prefix + ((size_t)bh * p.nseg + seg) * p.D * p.D;
+      if (p.transposed) {
+#pragma unroll
+        for (int j = 0; j < 128; ++j)
+          if (j < p.D) S[j] = src[(size_t)j * p.D + r];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j * 4 < p.D) {
+            const float4 x = *reinterpret_cast<const float4*>(src + (size_t)r * p.D + j * 4);
+            S[j * 4] = x.x; S[j * 4 + 1] = x.y; S[j * 4 + 2] = x.z; S[j * 4 + 3] = x.w;
+          }
+      }
+    }
+    publish();
+    bool ok = true;
+    for (int i = 0; i < nc; ++i) {
+      const int s = i & 1;
+      const bool last = i + 1 == nc;
+      const int rows = min(kRows, r_end - chunk_row(i));
+      const int t = kReverse ? rows - 1 - r : r;
+      const bool valid = r < rows;
+      const float w = valid ? p.sd * ex2(g2 * (float)(rows - t - p.e)) : 0.f;
+      ok = wait(kScores, i & 1) && wait(kCFull + s, (i >> 1) & 1);
+      if (!ok) break;
+      uint8_t* tb = sm + s * kRwStage + kTile;
+      if (!last) {
+#pragma unroll 4
+        for (int j = 0; j < 16; ++j) {
+          const uint32_t off = sw128_offset(r, j * 8, kRows);
+          uint4 x = *reinterpret_cast<uint4*>(tb + off), none;
+          if (!valid) x = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(tb + off) = scale8<false>(x, w, none);
+        }
+      }
+      if (!valid)  // padding may hold anything, and P's zeros must not meet it
+#pragma unroll 4
+        for (int j = 0; j < 16; ++j)
+          *reinterpret_cast<uint4*>(tb + kTile + sw128_offset(r, j * 8, kRows)) =
+              make_uint4(0, 0, 0, 0);
+      fence_async_smem();
+      mbar_arrive(&bars[kBReady]);
+      if (last) break;
+      const float keep = ex2(g2 * (float)rows);
+      ok = wait(kAddFull, i & 1);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {  // 16 columns at a time: S takes 128 of the 168 registers
+        uint32_t v[16];
+        tmem_ld16(tmem + lanes + kColAdd + q * 16, v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) S[q * 16 + j] = fmaf(keep, S[q * 16 + j], __uint_as_float(v[j]));
+      }
+      tc_fence_before();
+      ok = wait(kOFull, i & 1);  // a S of this chunk has read the copy
+      if (!ok) break;
+      publish();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace tc
+}  // namespace decay
+}  // namespace rehyat

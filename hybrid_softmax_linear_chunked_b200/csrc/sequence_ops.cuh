@@ -4,6 +4,7 @@
 #pragma once
 
 #include "decay.cuh"
+#include "decay_bf16.cuh"
 #include "rotary.cuh"
 
 namespace {
@@ -97,51 +98,115 @@ DecayPlan plan_decay(const rehyat_decay_args& a, bool backward) {
   return p;
 }
 
-template <typename T>
-int launch_decay_states_inst(const Pass& p, cudaStream_t st) {
-  auto k = rehyat::decay::decay_states_kernel<T>;
-  const int smem = rehyat::decay::states_smem_floats(rehyat::decay::padded(p.D)) * 4;
-  RH_TRY(cuda_check(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
-                    "decay states attr"));
-  k<<<dim3(p.nseg, p.B * p.H), rehyat::decay::kThreads, smem, st>>>(p);
-  return cuda_check(cudaGetLastError(), "decay states launch");
+// bf16 [B, heads, N, D] tensor with strides in elements, loaded and stored as 128-row x 64-column
+// boxes with 128-byte swizzle; columns past D read zeros and are not written.
+int make_map_rows(CUtensorMap* m, const void* base, const rehyat_strides& s, int D, int N,
+                  int heads, int B) {
+  EncodeTiledFn enc;
+  RH_TRY(get_encoder(&enc));
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)heads, (cuuint64_t)B};
+  // the stride of a single row, head or sequence is never used; any legal one will do
+  const long long one = D;
+  cuuint64_t strides[3] = {(cuuint64_t)(N > 1 ? s.row : one) * 2,
+                           (cuuint64_t)(heads > 1 ? s.head : one) * 2,
+                           (cuuint64_t)(B > 1 ? s.batch : one) * 2};
+  cuuint32_t box[4] = {64, 128, 1, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
+                   box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(REHYAT_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return REHYAT_OK;
 }
-int launch_decay_states(const Pass& p, rehyat_dtype dt, cudaStream_t st) {
-  return dt == REHYAT_BF16 ? launch_decay_states_inst<__nv_bfloat16>(p, st)
-                           : launch_decay_states_inst<float>(p, st);
+int map_of(CUtensorMap* m, const Rows& t, const Pass& p) {
+  return make_map_rows(m, t.p, rehyat_strides{t.sb, t.sh, t.sn}, p.D, p.N, p.H / t.group, p.B);
 }
 
-template <typename T, typename TOut>
-int launch_decay_rows_inst(const Pass& p, cudaStream_t st) {
-  auto k = rehyat::decay::decay_rows_kernel<T, TOut>;
-  const int smem = rehyat::decay::rows_smem_floats(rehyat::decay::padded(p.D)) * 4;
-  RH_TRY(cuda_check(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
-                    "decay rows attr"));
-  k<<<dim3(p.nseg, p.B * p.H), rehyat::decay::kThreads, smem, st>>>(p);
-  return cuda_check(cudaGetLastError(), "decay rows launch");
+// A launch behind another of the same call: with `behind`, it may start while that one still runs
+// (programmatic stream serialization) and waits for it before it reads what that one writes.
+struct Behind {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  Behind(dim3 grid, int threads, size_t smem, cudaStream_t st, bool behind) {
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = behind ? 1 : 0;
+  }
+};
+
+int launch_decay_states(const Pass& p, rehyat_dtype dt, cudaStream_t st) {
+  const dim3 grid(p.nseg, p.B * p.H);
+  if (dt == REHYAT_BF16) {
+    using namespace rehyat::decay::tc;
+    CUtensorMap mb, mc;
+    RH_TRY(map_of(&mb, p.b, p));
+    RH_TRY(map_of(&mc, p.c, p));
+    RH_TRY(cuda_check(cudaFuncSetAttribute(decay_states_bf16_kernel,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)kStSmem), "decay states attr"));
+    decay_states_bf16_kernel<<<grid, kStThreads, kStSmem, st>>>(mb, mc, p);
+  } else {
+    using namespace rehyat::decay;
+    const int smem = states_smem_floats(padded(p.D)) * 4;
+    RH_TRY(cuda_check(cudaFuncSetAttribute(decay_states_kernel,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
+                      "decay states attr"));
+    decay_states_kernel<<<grid, kThreads, smem, st>>>(p);
+  }
+  return cuda_check(cudaGetLastError(), "decay states launch");
 }
-int launch_decay_rows(const Pass& p, rehyat_dtype dt, bool out_f32, cudaStream_t st) {
-  if (dt == REHYAT_F32) return launch_decay_rows_inst<float, float>(p, st);
-  return out_f32 ? launch_decay_rows_inst<__nv_bfloat16, float>(p, st)
-                 : launch_decay_rows_inst<__nv_bfloat16, __nv_bfloat16>(p, st);
+
+// behind_scan: the launch before is this call's scan, whose prefix the kernel waits for.
+int launch_decay_rows(const Pass& p, rehyat_dtype dt, bool out_f32, bool behind_scan,
+                      cudaStream_t st) {
+  const dim3 grid(p.nseg, p.B * p.H);
+  if (dt == REHYAT_F32) {
+    using namespace rehyat::decay;
+    const int smem = rows_smem_floats(padded(p.D)) * 4;
+    RH_TRY(cuda_check(cudaFuncSetAttribute(decay_rows_kernel,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
+                      "decay rows attr"));
+    decay_rows_kernel<<<grid, kThreads, smem, st>>>(p);
+    return cuda_check(cudaGetLastError(), "decay rows launch");
+  }
+  using namespace rehyat::decay::tc;
+  CUtensorMap ma, mb, mc, mo;
+  RH_TRY(map_of(&ma, p.a, p));
+  RH_TRY(map_of(&mb, p.b, p));
+  RH_TRY(map_of(&mc, p.c, p));
+  mo = ma;  // unused with fp32 output
+  if (!out_f32) RH_TRY(make_map_rows(&mo, p.out, rehyat_strides{p.ob, p.oh, p.on}, p.D, p.N, p.H, p.B));
+  auto k = p.reverse ? (out_f32 ? decay_rows_bf16_kernel<true, true> : decay_rows_bf16_kernel<true, false>)
+                     : decay_rows_bf16_kernel<false, false>;
+  RH_TRY(cuda_check(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRwSmem),
+                    "decay rows attr"));
+  Behind l(grid, kRwThreads, kRwSmem, st, behind_scan);
+  return cuda_check(cudaLaunchKernelEx(&l.cfg, k, ma, mb, mc, mo, p), "decay rows launch");
 }
 
 int launch_decay_scan(const Pass& p, const float* S0, float* last, bool need_prefix,
-                      cudaStream_t st) {
+                      bool behind_states, cudaStream_t st) {
   const int n4 = p.D * p.D / 4;
-  rehyat::decay::decay_scan_kernel<<<dim3((n4 + 255) / 256, p.B * p.H), 256, 0, st>>>(
-      p.delta, S0, last, p.log_decay, p.lengths, p.H, p.N, p.D, p.nseg, p.seg_rows, p.reverse,
-      need_prefix);
-  return cuda_check(cudaGetLastError(), "decay scan launch");
+  Behind l(dim3((n4 + 255) / 256, p.B * p.H), 256, 0, st, behind_states);
+  return cuda_check(cudaLaunchKernelEx(&l.cfg, rehyat::decay::decay_scan_kernel, p.delta, S0, last,
+                                       p.log_decay, p.lengths, p.H, p.N, p.D, p.nseg, p.seg_rows,
+                                       p.reverse, (int)need_prefix),
+                    "decay scan launch");
 }
 
 // The state before every segment of a pass (rows b, c; time direction and e as in `p`) from `S0`
 // (or zero), and the state after the last into `last` unless null.  *prefix: where the row pass
-// reads it ([B*H][nseg][D][D]), null for zero.
+// reads it ([B*H][nseg][D][D]), null for zero.  *scanned: whether a scan was launched for them.
 int decay_prefix(Pass p, rehyat_dtype dt, const float* S0, float* last, const float** prefix,
-                 cudaStream_t st) {
-  const bool many = p.nseg > 1;
+                 bool* scanned, cudaStream_t st) {
+  const bool many = p.nseg > 1, bf16 = dt == REHYAT_BF16;
   *prefix = nullptr;
+  *scanned = false;
   if (!many && !last) {
     *prefix = S0;
     return REHYAT_OK;
@@ -151,8 +216,9 @@ int decay_prefix(Pass p, rehyat_dtype dt, const float* S0, float* last, const fl
     RH_TRY(launch_decay_states(p, dt, st));
   }
   // the row pass reads the workspace's copy of S0, since `last` may be S0
-  RH_TRY(launch_decay_scan(p, S0, last, many || S0, st));
+  RH_TRY(launch_decay_scan(p, S0, last, many || S0, bf16 && p.N > 0, st));
   if (many || S0) *prefix = p.delta;
+  *scanned = true;
   return REHYAT_OK;
 }
 
@@ -279,11 +345,12 @@ int rehyat_decay_forward(rehyat_decay_args a, rehyat_dtype dt, const void* q, re
   p.e = 1;
   p.sp = p.si = a.scale;
   p.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.fwd);
-  RH_TRY(decay_prefix(p, dt, S0, S_last, &p.prefix, st));
+  bool scanned;
+  RH_TRY(decay_prefix(p, dt, S0, S_last, &p.prefix, &scanned, st));
   if (a.N == 0) return REHYAT_OK;
   p.out = out;
   p.ob = so.batch; p.oh = so.head; p.on = so.row;
-  return launch_decay_rows(p, dt, false, st);
+  return launch_decay_rows(p, dt, false, scanned, st);
 }
 
 int rehyat_decay_backward(rehyat_decay_args a, rehyat_dtype dt, const void* q, rehyat_strides sq,
@@ -320,10 +387,11 @@ int rehyat_decay_backward(rehyat_decay_args a, rehyat_dtype dt, const void* q, r
   Pass f = decay_pass(a, log_decay, lengths, pl.seg);
   f.delta = reinterpret_cast<float*>(ws + pl.fwd);
   f.e = 1;
+  bool scanned = false;
   if (a.N > 0) {
     f.b = rk;
     f.c = rv;
-    RH_TRY(decay_prefix(f, dt, S0, nullptr, &f.prefix, st));
+    RH_TRY(decay_prefix(f, dt, S0, nullptr, &f.prefix, &scanned, st));
     f.a = rdo;
     f.b = rv;
     f.c = rk;
@@ -331,7 +399,7 @@ int rehyat_decay_backward(rehyat_decay_args a, rehyat_dtype dt, const void* q, r
     f.sp = f.si = a.scale;
     f.out = dq;
     f.ob = sdq.batch; f.oh = sdq.head; f.on = sdq.row;
-    RH_TRY(launch_decay_rows(f, dt, false, st));
+    RH_TRY(launch_decay_rows(f, dt, false, scanned, st));
   }
 
   // dK, dV: backward in time over the gradient of the state, sum of scale * q dO^T
@@ -342,7 +410,7 @@ int rehyat_decay_backward(rehyat_decay_args a, rehyat_dtype dt, const void* q, r
   r.b = rq;
   r.c = rdo;
   r.sp = r.sd = a.scale;
-  RH_TRY(decay_prefix(r, dt, dS_last, dS0, &r.prefix, st));
+  RH_TRY(decay_prefix(r, dt, dS_last, dS0, &r.prefix, &scanned, st));
   if (a.N == 0) return REHYAT_OK;
   float* part = reinterpret_cast<float*>(ws + pl.part);
   for (int i = 0; i < 2; ++i) {
@@ -356,12 +424,12 @@ int rehyat_decay_backward(rehyat_decay_args a, rehyat_dtype dt, const void* q, r
     if (group == 1) {
       p.out = dst;
       p.ob = s.batch; p.oh = s.head; p.on = s.row;
-      RH_TRY(launch_decay_rows(p, dt, false, st));
+      RH_TRY(launch_decay_rows(p, dt, false, scanned && i == 0, st));
       continue;
     }
     p.out = part;
     p.on = a.D; p.oh = (long long)a.N * a.D; p.ob = p.oh * a.H;
-    RH_TRY(launch_decay_rows(p, dt, true, st));
+    RH_TRY(launch_decay_rows(p, dt, true, scanned && i == 0, st));
     const long long vec = (long long)a.N * a.D / 4;
     const dim3 grid((unsigned)(vec / 1024 + 1 < 4096 ? vec / 1024 + 1 : 4096), a.B * a.Hk);
     if (dt == REHYAT_BF16)

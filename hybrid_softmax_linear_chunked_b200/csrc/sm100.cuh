@@ -197,6 +197,38 @@ __device__ __forceinline__ void tma_store_3d_chk(int site, const CUtensorMap* ma
 #endif
   tma_store_3d(map, src, c0, c1, c2);
 }
+// Four-dimensional tile load and store (column, row, head, sequence of a strided tensor), with the
+// checks of the three-dimensional ones in debug-bounds builds: the inner coordinate a multiple of
+// 8 elements below two 64-column boxes, row, head and sequence inside the tensor.
+__device__ __forceinline__ bool coord_4d_ok(int site, int c0, int c1, int c2, int c3, int ext1,
+                                            int ext2, int ext3) {
+#ifdef REHYAT_DEBUG_BOUNDS
+  return bounds_ok(site, c0 & 7, 0, 1) & bounds_ok(site, c0, 0, 128) &
+         bounds_ok(site, c1, 0, ext1) & bounds_ok(site, c2, 0, ext2) & bounds_ok(site, c3, 0, ext3);
+#else
+  (void)site, (void)c0, (void)c1, (void)c2, (void)c3, (void)ext1, (void)ext2, (void)ext3;
+  return true;
+#endif
+}
+__device__ __forceinline__ void tma_load_4d_chk(int site, void* dst, const CUtensorMap* map,
+                                                uint64_t* bar, int c0, int c1, int c2, int c3,
+                                                int ext1, int ext2, int ext3) {
+  if (!coord_4d_ok(site, c0, c1, c2, c3, ext1, ext2, ext3)) c0 = c1 = c2 = c3 = 0;
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_4d_chk(int site, const CUtensorMap* map, const void* src,
+                                                 int c0, int c1, int c2, int c3, int ext1,
+                                                 int ext2, int ext3) {
+  if (!coord_4d_ok(site, c0, c1, c2, c3, ext1, ext2, ext3)) return;
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];"
+      ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
 __device__ __forceinline__ void bulk_commit_group() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
