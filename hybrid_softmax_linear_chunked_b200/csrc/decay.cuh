@@ -219,14 +219,23 @@ __global__ void __launch_bounds__(256)
   if (S0) acc = reinterpret_cast<const float4*>(S0)[(size_t)bh * n4 + i];
   float4* d = reinterpret_cast<float4*>(delta) + (size_t)bh * nseg * n4 + i;
   const int steps = last ? nseg : nseg - 1;  // the last segment's sum is only in the last state
-#pragma unroll 4
-  for (int t = 0; t < nseg; ++t) {
-    const int s = reverse ? nseg - 1 - t : t;
-    const int rows = min(max(n - s * seg_rows, 0), seg_rows);
-    float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (t < steps && rows > 0) add = d[(size_t)s * n4];
-    if (need_prefix) d[(size_t)s * n4] = acc;
-    if (t < steps && rows > 0) acc = fma4(exp2f(g2 * (float)rows), acc, add);
+  // eight segments' sums are loaded before any is written over, so their latencies overlap
+  for (int t0 = 0; t0 < nseg; t0 += 8) {
+    float4 add[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int t = t0 + u, s = reverse ? nseg - 1 - t : t;
+      add[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t < steps && n > s * seg_rows) add[u] = d[(size_t)s * n4];
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int t = t0 + u, s = reverse ? nseg - 1 - t : t;
+      if (t >= nseg) break;
+      const int rows = min(max(n - s * seg_rows, 0), seg_rows);
+      if (need_prefix) d[(size_t)s * n4] = acc;
+      if (t < steps && rows > 0) acc = fma4(exp2f(g2 * (float)rows), acc, add[u]);
+    }
   }
   if (last) reinterpret_cast<float4*>(last)[(size_t)bh * n4 + i] = acc;
 }

@@ -42,19 +42,25 @@ __device__ __forceinline__ void load_tile(int site, uint8_t* dst, const CUtensor
   tma_load_4d_chk(site, dst, m, bar, 0, row, h, b, p.N, heads, p.B);
   tma_load_4d_chk(site, dst + kRows * 128, m, bar, 64, row, h, b, p.N, heads, p.B);
 }
+__device__ __forceinline__ uint64_t f2_bits(uint32_t lo, uint32_t hi) {
+  return f2_pack(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint32_t f2_bf16(uint64_t v) {
+  float a, b;
+  f2_unpack(v, a, b);
+  return pack_bf16x2(a, b);
+}
 // Eight bf16 values times w, rounded to bf16; with kTwo the rounding's remainder in a second part.
 template <bool kTwo>
 __device__ __forceinline__ uint4 scale8(uint4 x, float w, uint4& lo) {
   uint32_t in[4] = {x.x, x.y, x.z, x.w}, hi[4], rest[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&in[i]));
-    const float a = f.x * w, b = f.y * w;
-    hi[i] = pack_bf16x2(a, b);
-    if (kTwo) {
-      const float2 h = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&hi[i]));
-      rest[i] = pack_bf16x2(a - h.x, b - h.y);
-    }
+    // a bf16 is the upper half of an fp32
+    const uint64_t f = f2_mul(f2_bits(in[i] << 16, in[i] & 0xffff0000u), f2_pack(w, w));
+    hi[i] = f2_bf16(f);
+    if (kTwo)
+      rest[i] = f2_bf16(f2_fma(f2_bits(hi[i] << 16, hi[i] & 0xffff0000u), f2_pack(-1.f, -1.f), f));
   }
   if (kTwo) lo = make_uint4(rest[0], rest[1], rest[2], rest[3]);
   return make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -70,12 +76,21 @@ constexpr uint32_t kStOffLo = kStStages * 2 * kTile;
 constexpr uint32_t kStSmem = kStOffLo + kTile + 1024;
 static_assert(kStSmem + 256 <= 232448, "shared memory over the limit");
 
-// Every weight is taken to the segment's end, so all chunks add into one accumulator and nothing is
-// rescaled.  grid (nseg, B*H), block 320.
+// Every weight is taken to the segment's end, so chunks add up without rescaling, in any order.
+// They run in the order opposite to the row pass that follows: what was read last (and may still be
+// in L2) is read first there.  A chunk is weighed and multiplied in two halves of 64 rows, so that
+// the products of one run while the other is weighed (one half's remainders fit beside three
+// stages).  The tensor core's own accumulation truncates, which shows in fp32 sums over thousands
+// of rows (8.6e-6 of the state after 12,600 rows); every kFlush chunks the sum moves to registers.
+// grid (nseg, B*H), block 320.
+constexpr int kFlush = 8;
 __global__ void __launch_bounds__(kStThreads, 1)
     decay_states_bf16_kernel(const __grid_constant__ CUtensorMap tmB,
                              const __grid_constant__ CUtensorMap tmC, const Pass p) {
-  enum { kFull = 0, kEmpty = kFull + kStStages, kReady = kEmpty + kStStages, kLoFree, kDone, kNum };
+  enum {
+    kFull = 0, kEmpty = kFull + kStStages, kReady = kEmpty + kStStages, kLoFree = kReady + 2,
+    kDone = kLoFree + 2, kNum
+  };
   grid_dep_signal();
   const int seg = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh - b * p.H;
   if (seg == p.seg_skip) return;
@@ -95,7 +110,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
     tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < kNum; ++i) mbar_init(&bars[i], i == kReady ? kStMath : 1);
+    for (int i = 0; i < kNum; ++i) mbar_init(&bars[i], i == kReady || i == kReady + 1 ? kStMath : 1);
     abort_sh = 0;
     fence_mbar_init();
   }
@@ -106,6 +121,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
   auto wait = [&](int bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(&bars[bar], parity, abort_flag));
   };
+  auto chunk_row = [&](int i) { return r_begin + (p.reverse ? i : nc - 1 - i) * kRows; };
 
   if (warp == 8) {  // ---- copies ----
     const int hb = h / p.b.group, hc = h / p.c.group;
@@ -118,9 +134,8 @@ __global__ void __launch_bounds__(kStThreads, 1)
       if (lane == 0) {
         uint8_t* dst = sm + s * 2 * kTile;
         mbar_arrive_expect_tx(&bars[kFull + s], 2 * kTile);
-        load_tile(51, dst, &tmB, &bars[kFull + s], r_begin + i * kRows, hb, b, p, p.H / p.b.group);
-        load_tile(52, dst + kTile, &tmC, &bars[kFull + s], r_begin + i * kRows, hc, b, p,
-                  p.H / p.c.group);
+        load_tile(51, dst, &tmB, &bars[kFull + s], chunk_row(i), hb, b, p, p.H / p.b.group);
+        load_tile(52, dst + kTile, &tmC, &bars[kFull + s], chunk_row(i), hc, b, p, p.H / p.c.group);
       }
       __syncwarp();
       ++issued;
@@ -132,74 +147,97 @@ __global__ void __launch_bounds__(kStThreads, 1)
   } else if (warp == 9) {  // ---- products: b^T c, high and low part of b ----
     const int w = (p.D + 15) / 16 * 16;
     const uint32_t id = idesc_bf16(128, w, true, true);
-    const uint32_t lo = smem_u32(sm + kStOffLo);
+    const uint32_t sm0 = smem_u32(sm), lo = sm0 + kStOffLo, leader = elect_lane();
     bool ok = true;
     for (int i = 0; i < nc && ok; ++i) {
       const int s = i % kStStages;
-      ok = wait(kReady, i & 1);
-      if (!ok) break;
-      tc_fence_after();
-      if (lane == 0) {
-        const uint32_t hi = smem_u32(sm + s * 2 * kTile), c = hi + kTile;
-        for (int kk = 0; kk < kRows / 16; ++kk) {
-          mma_ss(tmem, mnmajor_desc(hi, kk), mnmajor_desc(c, kk), id, (i > 0 || kk > 0) ? 1u : 0u);
-          mma_ss(tmem, mnmajor_desc(lo, kk), mnmajor_desc(c, kk), id, 1u);
+      for (int half = 0; half < 2 && ok; ++half) {
+        ok = wait(kReady + half, i & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t hi = sm0 + s * 2 * kTile, c = hi + kTile;
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4) {
+          const int kk = half * 4 + k4;
+          mma_ss_by(leader, tmem, mnmajor_desc(hi, kk), mnmajor_desc(c, kk), id,
+                    (i % kFlush > 0 || kk > 0) ? 1u : 0u);
+          mma_ss_by(leader, tmem, mnmajor_desc(lo, kk), mnmajor_desc(c, kk), id, 1u);
         }
-        mma_commit(&bars[kLoFree]);
-        mma_commit(&bars[kEmpty + s]);
+        mma_commit_by(leader, &bars[kLoFree + half]);
+        if (half) mma_commit_by(leader, &bars[kEmpty + s]);
+        __syncwarp();
       }
-      __syncwarp();
     }
-    if (lane == 0) mma_commit(&bars[kDone]);
+    mma_commit_by(leader, &bars[kDone]);
     __syncwarp();
     mbar_wait_drain(&bars[kDone], 0);
     __syncwarp();
-  } else {  // ---- weights: row r, columns half by half ----
-    const int r = tid & 127, half = tid >> 7;
+  } else {  // ---- weights: a row of a half chunk, 32 columns a thread ----
+    const int r64 = tid & 63, c0 = (tid >> 6) * 32;
     const float g2 = log2_decay(p.log_decay, h);
+    // the sum: row (TMEM lane) rs, columns cs .. cs + 63
+    const int rs = tid & 127, cs = (tid >> 7) * 64;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    float sum[64];
+#pragma unroll
+    for (int j = 0; j < 64; ++j) sum[j] = 0.f;
+    auto flush = [&]() {
+      tc_fence_after();
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t v[32];
+        tmem_ld32(tmem + lanes + cs + q * 32, v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) sum[q * 32 + j] += __uint_as_float(v[j]);
+      }
+      tc_fence_before();
+    };
     bool ok = true;
-    for (int i = 0; i < nc; ++i) {
+    for (int i = 0; i < nc && ok; ++i) {
       const int s = i % kStStages;
       ok = wait(kFull + s, (i / kStStages) & 1);
-      if (ok && i > 0) ok = wait(kLoFree, (i - 1) & 1);
-      if (!ok) break;
-      const int row = r_begin + i * kRows + r;
-      const bool valid = row < r_end;
-      const int m = p.reverse ? row - r_begin + 1 - p.e : r_end - p.e - row;
-      const float w = valid ? p.sd * exp2f(g2 * (float)m) : 0.f;
+      if (ok && i > 0 && i % kFlush == 0) {
+        ok = wait(kLoFree + 1, (i - 1) & 1);  // the products of every chunk before are complete
+        if (ok) flush();
+      }
       uint8_t* hi = sm + s * 2 * kTile;
       uint8_t* lo = sm + kStOffLo;
+#pragma unroll 1
+      for (int half = 0; half < 2 && ok; ++half) {
+        const int r = half * 64 + r64, row = chunk_row(i) + r;
+        const bool valid = row < r_end;
+        const int m = p.reverse ? row - r_begin + 1 - p.e : r_end - p.e - row;
+        const float w = valid ? p.sd * exp2f(g2 * (float)m) : 0.f;
+        uint4 x[4], rest[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t off = sw128_offset(r, half * 64 + j * 8, kRows);
-        uint4 x = *reinterpret_cast<uint4*>(hi + off), rest;
-        if (!valid) x = make_uint4(0, 0, 0, 0);  // padding may hold anything
-        x = scale8<true>(x, w, rest);
-        *reinterpret_cast<uint4*>(hi + off) = x;
-        *reinterpret_cast<uint4*>(lo + off) = rest;
-        if (!valid) *reinterpret_cast<uint4*>(hi + kTile + off) = make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < 4; ++j) {
+          x[j] = *reinterpret_cast<uint4*>(hi + sw128_offset(r, c0 + j * 8, kRows));
+          if (!valid) x[j] = make_uint4(0, 0, 0, 0);  // padding may hold anything
+          x[j] = scale8<true>(x[j], w, rest[j]);
+        }
+        if (i > 0) ok = wait(kLoFree + half, (i - 1) & 1);
+        if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t off = sw128_offset(r, c0 + j * 8, kRows);
+          *reinterpret_cast<uint4*>(hi + off) = x[j];
+          *reinterpret_cast<uint4*>(lo + off) = rest[j];
+          if (!valid) *reinterpret_cast<uint4*>(hi + kTile + off) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_smem();
+        mbar_arrive(&bars[kReady + half]);
       }
-      fence_async_smem();
-      mbar_arrive(&bars[kReady]);
     }
     if (ok) ok = wait(kDone, 0);
     if (ok) {
-      tc_fence_after();
-      float* dst = p.delta + (((size_t)bh * p.nseg + seg) * p.D + r) * p.D;
+      flush();
+      float* dst = p.delta + (((size_t)bh * p.nseg + seg) * p.D + rs) * p.D;
+      if (rs < p.D) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int c0 = half * 64 + q * 32;
-        if (c0 >= p.D) break;
-        uint32_t v[32];
-        tmem_ld32(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0, v);
-        if (r < p.D) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (c0 + j * 4 < p.D)
-              *reinterpret_cast<float4*>(dst + c0 + j * 4) =
-                  make_float4(__uint_as_float(v[j * 4]), __uint_as_float(v[j * 4 + 1]),
-                              __uint_as_float(v[j * 4 + 2]), __uint_as_float(v[j * 4 + 3]));
-        }
+        for (int j = 0; j < 16; ++j)
+          if (cs + j * 4 < p.D)
+            *reinterpret_cast<float4*>(dst + cs + j * 4) =
+                make_float4(sum[j * 4], sum[j * 4 + 1], sum[j * 4 + 2], sum[j * 4 + 3]);
       }
     }
   }
@@ -214,8 +252,11 @@ __global__ void __launch_bounds__(kStThreads, 1)
 // ---------------------------------------------------------------------------------------------
 // Rows.
 // ---------------------------------------------------------------------------------------------
-// warps 0-3: scores and outputs, 4-7: weights and the state, 8: copies in, 9: products, 10: copies out
-constexpr int kRwThreads = 352;
+// warps 0-7: scores and outputs, 8-15: weights and the state (of each, four warps take columns 0-63
+// and four 64-127), 16: copies in, 17: products, 18: copies out.  With four warps for each of the
+// first two the chains between the products took 8,800 clk a chunk, 5,600 more than the products.
+constexpr int kRwThreads = 608;
+constexpr int kRwIn = 16, kRwMma = 17, kRwOut = 18;
 constexpr uint32_t kRwStage = 3 * kTile;
 constexpr uint32_t kRwOffS = 2 * kRwStage;
 constexpr uint32_t kRwSmem = kRwOffS + kTile + 1024;
@@ -224,12 +265,12 @@ static_assert(kRwSmem + 512 <= 232448, "shared memory over the limit");
 constexpr uint32_t kColP = 0, kColIn = 128, kColSt = 256, kColAdd = 384;
 
 // A chunk i, chunk after chunk in time order:
-//   scores = a b^T -> P = sp L^|i-j| scores on the past, bf16, into TMEM     (warps 0-3)
-//   b weighted in place (after the scores have read it)                       (warps 4-7)
-//   add = b^T c;  in = P c;  st = a S                                         (warp 9)
-//   out = in + si L^(t+e) st -> over a's tile -> global                       (warps 0-3, 10)
-//   S = L^rows S + add, in registers (a row a thread), bf16 copy for a S      (warps 4-7)
-// grid (nseg, B*H), block 352.
+//   scores = a b^T -> P = sp L^|i-j| scores on the past, bf16, into TMEM     (warps 0-7)
+//   b weighted in place (after the scores have read it)                       (warps 8-15)
+//   add = b^T c;  in = P c;  st = a S                                         (warp 17)
+//   out = in + si L^(t+e) st -> over a's tile -> global                       (warps 0-7, 18)
+//   S = L^rows S + add, in registers (half a row a thread), bf16 copy for a S (warps 8-15)
+// grid (nseg, B*H), block 608.
 template <bool kReverse, bool kOutF32>
 __global__ void __launch_bounds__(kRwThreads, 1)
     decay_rows_bf16_kernel(const __grid_constant__ CUtensorMap tmA,
@@ -268,14 +309,14 @@ __global__ void __launch_bounds__(kRwThreads, 1)
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
   volatile int* abort_flag = &abort_sh;
-  if (warp == 8) {
+  if (warp == kRwIn) {
     tmem_alloc(&tmem_sh, 512);
     tmem_relinquish();
   }
   if (tid == 0) {
     for (int i = 0; i < kNum; ++i) {
       const bool many = i == kPReady || i == kBReady || i == kOFree || i == kSReady || i == kStaged;
-      mbar_init(&bars[i], many ? 128 : 1);
+      mbar_init(&bars[i], many ? 256 : 1);
     }
     abort_sh = 0;
     fence_mbar_init();
@@ -289,7 +330,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
     return __all_sync(0xffffffffu, mbar_wait(&bars[bar], parity, abort_flag));
   };
 
-  if (warp == 8) {  // ---- copies in ----
+  if (warp == kRwIn) {  // ---- copies in ----
     const int hb = h / p.b.group, hc = h / p.c.group, ha = h / p.a.group;
     if (lane == 0) {
       tma_prefetch_desc(&tmA);
@@ -326,23 +367,23 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       drain(kCFull, n_c);
     }
     __syncwarp();
-  } else if (warp == 9) {  // ---- products ----
+  } else if (warp == kRwMma) {  // ---- products ----
     const int kd = (p.D + 15) / 16, w = kd * 16;
     const uint32_t id_p = idesc_bf16(128, 128, false, false);  // a (K-major) x b (K-major)
     const uint32_t id_o = idesc_bf16(128, w, false, true);     // P or a x c or S (N-major)
     const uint32_t id_s = idesc_bf16(128, w, true, true);      // b^T x c
-    const uint32_t sS = smem_u32(sm + kRwOffS);
-    auto tile = [&](int i, int slot) { return smem_u32(sm + (i & 1) * kRwStage + slot * kTile); };
+    const uint32_t sm0 = smem_u32(sm), sS = sm0 + kRwOffS, leader = elect_lane();
+    auto tile = [&](int i, int slot) { return sm0 + (i & 1) * kRwStage + slot * kTile; };
     auto scores = [&](int i) {
       bool ok = wait(kAFull + (i & 1), (i >> 1) & 1) && wait(kBFull + (i & 1), (i >> 1) & 1);
       if (!ok) return false;
       tc_fence_after();
-      if (lane == 0) {
-        for (int kk = 0; kk < kd; ++kk)
-          mma_ss(tmem + kColP, kmajor_desc(tile(i, 0), kk), kmajor_desc(tile(i, 1), kk), id_p,
-                 kk > 0 ? 1u : 0u);
-        mma_commit(&bars[kScores]);
-      }
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        if (kk < kd)
+          mma_ss_by(leader, tmem + kColP, kmajor_desc(tile(i, 0), kk), kmajor_desc(tile(i, 1), kk),
+                    id_p, kk > 0 ? 1u : 0u);
+      mma_commit_by(leader, &bars[kScores]);
       __syncwarp();
       return true;
     };
@@ -354,39 +395,40 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       ok = wait(kCFull + s, (i >> 1) & 1) && wait(kBReady, i & 1);
       if (!ok) break;
       tc_fence_after();
-      if (lane == 0) {
-        if (!last) {
-          for (int kk = 0; kk < kRows / 16; ++kk)
-            mma_ss(tmem + kColAdd, mnmajor_desc(tile(i, 1), kk), mnmajor_desc(tile(i, 2), kk), id_s,
-                   kk > 0 ? 1u : 0u);
-          mma_commit(&bars[kAddFull]);
-        }
-        mma_commit(&bars[kBEmpty + s]);
+      if (!last) {
+#pragma unroll
+        for (int kk = 0; kk < kRows / 16; ++kk)
+          mma_ss_by(leader, tmem + kColAdd, mnmajor_desc(tile(i, 1), kk),
+                    mnmajor_desc(tile(i, 2), kk), id_s, kk > 0 ? 1u : 0u);
+        mma_commit_by(leader, &bars[kAddFull]);
       }
+      mma_commit_by(leader, &bars[kBEmpty + s]);
       __syncwarp();
       ok = wait(kPReady, i & 1) && wait(kSReady, i & 1);
       if (ok && i > 0) ok = wait(kOFree, (i - 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      if (lane == 0) {
-        for (int kk = 0; kk < kRows / 16; ++kk)
-          mma_ts(tmem + kColIn, tmem + kColP + kk * 8, mnmajor_desc(tile(i, 2), kk), id_o,
-                 kk > 0 ? 1u : 0u);
-        mma_commit(&bars[kCEmpty + s]);
-        if (reads_state)
-          for (int kk = 0; kk < kd; ++kk)
-            mma_ss(tmem + kColSt, kmajor_desc(tile(i, 0), kk), mnmajor_desc(sS, kk), id_o,
-                   kk > 0 ? 1u : 0u);
-        mma_commit(&bars[kOFull]);
+#pragma unroll
+      for (int kk = 0; kk < kRows / 16; ++kk)
+        mma_ts_by(leader, tmem + kColIn, tmem + kColP + (kk >> 2) * 64 + (kk & 3) * 8,
+                  mnmajor_desc(tile(i, 2), kk), id_o, kk > 0 ? 1u : 0u);
+      mma_commit_by(leader, &bars[kCEmpty + s]);
+      if (reads_state) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          if (kk < kd)
+            mma_ss_by(leader, tmem + kColSt, kmajor_desc(tile(i, 0), kk), mnmajor_desc(sS, kk), id_o,
+                      kk > 0 ? 1u : 0u);
       }
+      mma_commit_by(leader, &bars[kOFull]);
       __syncwarp();
       if (!last) ok = scores(i + 1);
     }
-    if (lane == 0) mma_commit(&bars[kDone]);
+    mma_commit_by(leader, &bars[kDone]);
     __syncwarp();
     mbar_wait_drain(&bars[kDone], 0);
     __syncwarp();
-  } else if (warp == 10) {  // ---- copies out; a's tile is free once its output has left ----
+  } else if (warp == kRwOut) {  // ---- copies out; a's tile is free once its output has left ----
     bool ok = true;
     for (int i = 0; i < nc && ok; ++i) {
       ok = wait(kStaged, i & 1);
@@ -406,48 +448,58 @@ __global__ void __launch_bounds__(kRwThreads, 1)
     }
     if (!kOutF32 && lane == 0) bulk_wait_all();
     __syncwarp();
-  } else if (warp < 4) {  // ---- scores and outputs: row r of the chunk = TMEM lane ----
-    const int r = tid;
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+  } else if (warp < 8) {  // ---- scores and outputs: row r of the chunk = TMEM lane ----
+    const int r = tid & 127, half = warp >> 2, rw = warp & 3;
+    const uint32_t lanes = static_cast<uint32_t>(rw * 32) << 16;
     const float g2 = log2_decay(p.log_decay, h);
-    // L^|i-j| off the diagonal 32 x 32 blocks = (power of the row to the block's near edge) x
-    // (power within the block), both exponents >= 0; on the diagonal one power an element
-    float in_block[32];
+    // L^|i-j| off the diagonal 32 x 32 blocks = (power of the row to the near edge of 16 columns)
+    // x (power within them), both exponents >= 0; on the diagonal one power an element
+    uint64_t within[8];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) in_block[j] = ex2(g2 * (float)(kReverse ? j : 31 - j));
+    for (int j = 0; j < 8; ++j)
+      within[j] = f2_pack(ex2(g2 * (float)(kReverse ? 2 * j : 15 - 2 * j)),
+                          ex2(g2 * (float)(kReverse ? 2 * j + 1 : 14 - 2 * j)));
     bool ok = true;
     for (int i = 0; i < nc; ++i) {
       const int row0 = chunk_row(i), rows = min(kRows, r_end - row0);
       ok = wait(kScores, i & 1);
       if (!ok) break;
       tc_fence_after();
+      // 16 columns a turn; a warp's P (64 columns' bf16 pairs: 32 TMEM columns) lies over its own
+      // half of the scores, behind the columns already read
 #pragma unroll 1
-      for (int jb = 0; jb < 4; ++jb) {
-        uint32_t pk[16];
-        if (kReverse ? jb < warp : jb > warp) {  // no past here
+      for (int e = 0; e < 4; ++e) {
+        const int c0 = half * 64 + e * 16, jb = c0 >> 5;
+        uint32_t pk[8];
+        if (kReverse ? jb < rw : jb > rw) {  // no past here
 #pragma unroll
-          for (int j = 0; j < 16; ++j) pk[j] = 0u;
+          for (int j = 0; j < 8; ++j) pk[j] = 0u;
         } else {
-          uint32_t v[32];
-          tmem_ld32(tmem + lanes + kColP + jb * 32, v);
-          float f[32];
-          if (jb == warp || (kReverse && rows < kRows)) {
+          uint32_t v[16];
+          tmem_ld16(tmem + lanes + kColP + c0, v);
+          if (jb == rw || (kReverse && rows < kRows)) {
+            const int d0 = kReverse ? c0 - r : r - c0;
+            const int stop = rows - c0;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const int c = jb * 32 + j, d = kReverse ? c - r : r - c;
-              const bool past = d >= 0 && c < rows;
-              f[j] = past ? p.sp * ex2(g2 * (float)d) * __uint_as_float(v[j]) : 0.f;
+            for (int j = 0; j < 8; ++j) {
+              float f[2];
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const int c = 2 * j + u, d = kReverse ? d0 + c : d0 - c;
+                const float x = p.sp * ex2(g2 * (float)d) * __uint_as_float(v[c]);
+                f[u] = d >= 0 && (!kReverse || c < stop) ? x : 0.f;
+              }
+              pk[j] = pack_bf16x2(f[0], f[1]);
             }
           } else {
-            const int d = kReverse ? jb * 32 - r : r - jb * 32 - 31;
-            const float edge = p.sp * ex2(g2 * (float)d);
+            const float edge = p.sp * ex2(g2 * (float)(kReverse ? c0 - r : r - c0 - 15));
+            const uint64_t edge2 = f2_pack(edge, edge);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) f[j] = edge * in_block[j] * __uint_as_float(v[j]);
+            for (int j = 0; j < 8; ++j)
+              pk[j] = f2_bf16(f2_mul(f2_mul(edge2, within[j]), f2_bits(v[2 * j], v[2 * j + 1])));
           }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
         }
-        tmem_st16(tmem + lanes + kColP + jb * 16, pk);
+        tmem_st8(tmem + lanes + kColP + half * 64 + e * 8, pk);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -457,42 +509,48 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       const int t = kReverse ? rows - 1 - r : r;
       const bool valid = r < rows;
       const float f = p.si * ex2(g2 * (float)(max(t, 0) + p.e));
+      const uint64_t f2 = f2_pack(f, f);
       ok = wait(kOFull, i & 1);
       if (!ok) break;
       tc_fence_after();
       uint8_t* stage = sm + (i & 1) * kRwStage;
       float* of = kOutF32 ? static_cast<float*>(p.out) + b * p.ob + h * p.oh + (row0 + r) * p.on
                           : nullptr;
-      const int blocks = (p.D + 31) / 32;
+      const int c_end = min(half * 64 + 64, p.D);
 #pragma unroll 1
-      for (int cb = 0; cb < blocks; ++cb) {
-        uint32_t v[32];
-        float o[32];
-        tmem_ld32(tmem + lanes + kColIn + cb * 32, v);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(v[j]);
+      for (int c0 = half * 64; c0 < c_end; c0 += 16) {
+        uint64_t o[8];
         if (reads_state) {
-          tmem_ld32(tmem + lanes + kColSt + cb * 32, v);
+          uint32_t v[32];
+          tmem_ld16_pair(tmem + lanes + kColIn + c0, tmem + lanes + kColSt + c0, v);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = fmaf(f, __uint_as_float(v[j]), o[j]);
+          for (int j = 0; j < 8; ++j)
+            o[j] = f2_fma(f2, f2_bits(v[16 + 2 * j], v[17 + 2 * j]), f2_bits(v[2 * j], v[2 * j + 1]));
+        } else {
+          uint32_t v[16];
+          tmem_ld16(tmem + lanes + kColIn + c0, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j] = f2_bits(v[2 * j], v[2 * j + 1]);
         }
         if (!valid)
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = 0.f;
+          for (int j = 0; j < 8; ++j) o[j] = 0ull;
         if (kOutF32) {
           if (row0 + r < r_stop)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (cb * 32 + j * 4 < p.D)
-                *reinterpret_cast<float4*>(of + cb * 32 + j * 4) =
-                    make_float4(o[j * 4], o[j * 4 + 1], o[j * 4 + 2], o[j * 4 + 3]);
+            for (int j = 0; j < 4; ++j)
+              if (c0 + j * 4 < p.D) {
+                float4 x;
+                f2_unpack(o[2 * j], x.x, x.y);
+                f2_unpack(o[2 * j + 1], x.z, x.w);
+                *reinterpret_cast<float4*>(of + c0 + j * 4) = x;
+              }
         } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4*>(stage + sw128_offset(r, cb * 32 + j * 8, kRows)) =
-                make_uint4(pack_bf16x2(o[j * 8], o[j * 8 + 1]), pack_bf16x2(o[j * 8 + 2], o[j * 8 + 3]),
-                           pack_bf16x2(o[j * 8 + 4], o[j * 8 + 5]),
-                           pack_bf16x2(o[j * 8 + 6], o[j * 8 + 7]));
+          for (int j = 0; j < 2; ++j)
+            *reinterpret_cast<uint4*>(stage + sw128_offset(r, c0 + j * 8, kRows)) =
+                make_uint4(f2_bf16(o[4 * j]), f2_bf16(o[4 * j + 1]), f2_bf16(o[4 * j + 2]),
+                           f2_bf16(o[4 * j + 3]));
         }
       }
       tc_fence_before();
@@ -501,19 +559,18 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       mbar_arrive(&bars[kStaged]);
     }
   } else {  // ---- weights and the state: row r of b's tile, and row r of S = TMEM lane ----
-    const int r = tid & 127;
+    const int r = tid & 127, c0 = ((warp - 8) >> 2) * 64;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float g2 = log2_decay(p.log_decay, h);
     uint8_t* sS = sm + kRwOffS;
-    float S[128];
+    uint64_t S[32];  // pairs of columns
 #pragma unroll
-    for (int j = 0; j < 128; ++j) S[j] = 0.f;
+    for (int j = 0; j < 32; ++j) S[j] = 0ull;
     auto publish = [&]() {  // bf16 copy of S for the next chunk's a S
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        *reinterpret_cast<uint4*>(sS + sw128_offset(r, j * 8, kRows)) = make_uint4(
-            pack_bf16x2(S[j * 8], S[j * 8 + 1]), pack_bf16x2(S[j * 8 + 2], S[j * 8 + 3]),
-            pack_bf16x2(S[j * 8 + 4], S[j * 8 + 5]), pack_bf16x2(S[j * 8 + 6], S[j * 8 + 7]));
+      for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<uint4*>(sS + sw128_offset(r, c0 + j * 8, kRows)) = make_uint4(
+            f2_bf16(S[j * 4]), f2_bf16(S[j * 4 + 1]), f2_bf16(S[j * 4 + 2]), f2_bf16(S[j * 4 + 3]));
       fence_async_smem();
       mbar_arrive(&bars[kSReady]);
     };
@@ -522,14 +579,16 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       const float* src = p.prefix + ((size_t)bh * p.nseg + seg) * p.D * p.D;
       if (p.transposed) {
 #pragma unroll
-        for (int j = 0; j < 128; ++j)
-          if (j < p.D) S[j] = src[(size_t)j * p.D + r];
+        for (int j = 0; j < 32; ++j)
+          if (c0 + 2 * j < p.D)
+            S[j] = f2_pack(src[(size_t)(c0 + 2 * j) * p.D + r], src[(size_t)(c0 + 2 * j + 1) * p.D + r]);
       } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j * 4 < p.D) {
-            const float4 x = *reinterpret_cast<const float4*>(src + (size_t)r * p.D + j * 4);
-            S[j * 4] = x.x; S[j * 4 + 1] = x.y; S[j * 4 + 2] = x.z; S[j * 4 + 3] = x.w;
+        for (int j = 0; j < 16; ++j)
+          if (c0 + j * 4 < p.D) {
+            const float4 x = *reinterpret_cast<const float4*>(src + (size_t)r * p.D + c0 + j * 4);
+            S[j * 2] = f2_pack(x.x, x.y);
+            S[j * 2 + 1] = f2_pack(x.z, x.w);
           }
       }
     }
@@ -542,46 +601,48 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       const int t = kReverse ? rows - 1 - r : r;
       const bool valid = r < rows;
       const float w = valid ? p.sd * ex2(g2 * (float)(rows - t - p.e)) : 0.f;
+      uint8_t* tb = sm + s * kRwStage + kTile;
       ok = wait(kScores, i & 1) && wait(kCFull + s, (i >> 1) & 1);
       if (!ok) break;
-      uint8_t* tb = sm + s * kRwStage + kTile;
       if (!last) {
-#pragma unroll 4
-        for (int j = 0; j < 16; ++j) {
-          const uint32_t off = sw128_offset(r, j * 8, kRows);
-          uint4 x = *reinterpret_cast<uint4*>(tb + off), none;
-          if (!valid) x = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(tb + off) = scale8<false>(x, w, none);
+#pragma unroll 1
+        for (int c = c0; c < c0 + 64; c += 16) {
+          uint4* q0 = reinterpret_cast<uint4*>(tb + sw128_offset(r, c, kRows));
+          uint4* q1 = reinterpret_cast<uint4*>(tb + sw128_offset(r, c + 8, kRows));
+          uint4 x = *q0, y = *q1, none;
+          if (!valid) x = y = make_uint4(0, 0, 0, 0);
+          *q0 = scale8<false>(x, w, none);
+          *q1 = scale8<false>(y, w, none);
         }
       }
       if (!valid)  // padding may hold anything, and P's zeros must not meet it
-#pragma unroll 4
-        for (int j = 0; j < 16; ++j)
-          *reinterpret_cast<uint4*>(tb + kTile + sw128_offset(r, j * 8, kRows)) =
-              make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+        for (int c = c0; c < c0 + 64; c += 8)
+          *reinterpret_cast<uint4*>(tb + kTile + sw128_offset(r, c, kRows)) = make_uint4(0, 0, 0, 0);
       fence_async_smem();
       mbar_arrive(&bars[kBReady]);
       if (last) break;
       const float keep = ex2(g2 * (float)rows);
-      ok = wait(kAddFull, i & 1);
+      const uint64_t keep2 = f2_pack(keep, keep);
+      // also waits until a S of this chunk has read the copy
+      ok = wait(kAddFull, i & 1) && wait(kOFull, i & 1);
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {  // 16 columns at a time: S takes 128 of the 168 registers
+      for (int q = 0; q < 4; ++q) {
         uint32_t v[16];
-        tmem_ld16(tmem + lanes + kColAdd + q * 16, v);
+        tmem_ld16(tmem + lanes + kColAdd + c0 + q * 16, v);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) S[q * 16 + j] = fmaf(keep, S[q * 16 + j], __uint_as_float(v[j]));
+        for (int j = 0; j < 8; ++j)
+          S[q * 8 + j] = f2_fma(keep2, S[q * 8 + j], f2_bits(v[2 * j], v[2 * j + 1]));
       }
       tc_fence_before();
-      ok = wait(kOFull, i & 1);  // a S of this chunk has read the copy
-      if (!ok) break;
       publish();
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kRwIn) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
