@@ -7,8 +7,10 @@ library's CUDA kernels.  There is no CPU fallback: without the built library eve
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
+import struct
 
 import torch
 
@@ -46,22 +48,12 @@ class Dims(ctypes.Structure):
                 ("G", ctypes.c_int), ("P", ctypes.c_int), ("phi", ctypes.c_int)]
 
 
-class Strides(ctypes.Structure):
-    """Elements between two sequences, heads and rows of a [B, heads, N, D] tensor."""
-    _fields_ = [("batch", ctypes.c_longlong), ("head", ctypes.c_longlong),
-                ("row", ctypes.c_longlong)]
-
-
-class RotaryArgs(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_int) for n in ("B", "n", "Hq", "Hk", "D", "R", "interleaved",
-                                            "inverse", "axes", "pos64", "add_index")] + \
-        [(n, ctypes.c_longlong) for n in ("pos_axis", "pos_batch", "pos_token", "start")] + \
-        [("scale", ctypes.c_float)]
-
-
-class DecayArgs(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_int) for n in ("B", "H", "Hk", "N", "D")] + \
-        [("scale", ctypes.c_float)]
+# Argument blocks of the sequence operators (rehyat_*_args in include/rehyat.h).  A tensor of rows is
+# four 64-bit values: pointer and the strides of sequence, head and row.
+_ROTARY = struct.Struct("12i 7q 16q f4x")
+_DECAY_FORWARD = struct.Struct("6i 16q 6q f4x")
+_DECAY_BACKWARD = struct.Struct("6i 28q 7q f4x")
+_DECAY_STEP = struct.Struct("6i 16q 3q f4x")
 
 
 _lib = None
@@ -135,14 +127,9 @@ def load() -> ctypes.CDLL:
     L.rehyat_selftest_wait_timeout.argtypes = [ctypes.c_longlong, P]
     L.rehyat_selftest_bounds.argtypes = [P, ctypes.c_longlong, ctypes.c_longlong, P]
     L.rehyat_debug_bounds.argtypes = []
-    SP = [P, Strides]  # a strided tensor
-    L.rehyat_rotary.argtypes = [RotaryArgs, c_int] + SP * 2 + [P, P, P] + SP * 2 + [P]
-    L.rehyat_decay_workspace_size.argtypes = [DecayArgs, c_int, c_int, ctypes.POINTER(c_size_t)]
-    L.rehyat_decay_forward.argtypes = [DecayArgs, c_int] + SP * 3 + [P, P, P] + SP + \
-        [P, P, c_size_t, P]
-    L.rehyat_decay_backward.argtypes = [DecayArgs, c_int] + SP * 3 + [P, P, P] + SP + [P] + \
-        SP * 3 + [P, P, c_size_t, P]
-    L.rehyat_decay_step.argtypes = [DecayArgs, c_int] + SP * 3 + [P, P, c_int, P] + SP + [P]
+    for name in ("rotary", "decay_forward", "decay_backward", "decay_step"):
+        getattr(L, "rehyat_" + name).argtypes = [ctypes.c_char_p, P]
+    L.rehyat_decay_workspace_size.argtypes = [c_int] * 6 + [ctypes.POINTER(c_size_t)]
     L.rehyat_sync_status.argtypes = [P]
     for name in EXPORTED:
         if name not in ("rehyat_last_error",):
@@ -662,33 +649,45 @@ def sync_status(device: torch.device | None = None) -> None:
 # These calls read tensors by their strides: [B, heads, N, D] with contiguous rows of D, so a
 # transposed [B, N, heads, D] projection or a slice of a packed qkv needs no copy.
 
-def _strided(t: torch.Tensor, dev: torch.device, dtype: torch.dtype, shape, what: str):
-    """(pointer, strides) of a [B, heads, N, D] tensor for the library."""
-    if t.device != dev or dev.type != "cuda":
-        raise ValueError("all tensors must be on the same CUDA device")
-    if t.dtype != dtype:
-        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    st = t.stride()
-    if st[3] != 1 and shape[3] > 1:
+def _rows(t: torch.Tensor, like: torch.Tensor, shape, what: str):
+    """(pointer, strides of sequence, head and row) of a tensor of rows of this shape, of the type
+    and on the device of `like`."""
+    if t.dtype is not like.dtype or t.shape != shape or t.device != like.device:
+        _refuse(t, like.device, like.dtype, shape, what)
+    b, h, n, d = t.stride()
+    if d != 1 and shape[3] > 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
-    return t.data_ptr(), Strides(st[0], st[1], st[2])
+    return t.data_ptr(), b, h, n
 
 
-def _small(t: torch.Tensor | None, dev: torch.device, dtype: torch.dtype, shape, what: str):
+def _small(t: torch.Tensor | None, dev: torch.device, dtype: torch.dtype, shape, what: str) -> int:
     """Pointer of an optional contiguous tensor of the given type and shape."""
     if t is None:
-        return None
+        return 0
+    if t.dtype is not dtype or t.shape != shape or t.device != dev:
+        _refuse(t, dev, dtype, shape, what)
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _refuse(t, dev, dtype, shape, what) -> None:
     if t.device != dev:
         raise ValueError("all tensors must be on the same CUDA device")
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _cuda(dev: torch.device) -> torch.device:
+    if dev.type != "cuda":
+        raise ValueError("all tensors must be on the same CUDA device")
+    return dev
+
+
+# (torch.cuda.current_stream builds a Stream object: 2 us of a step's 10)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _scratch(nbytes: int, dev: torch.device, workspace: torch.Tensor | None) -> torch.Tensor:
@@ -698,15 +697,14 @@ def _scratch(nbytes: int, dev: torch.device, workspace: torch.Tensor | None) -> 
     return _workspace(nbytes, dev, workspace)
 
 
-def _call(dev: torch.device, fn, *args) -> None:
+def _call(dev: torch.device, fn, block: bytes) -> None:
     """Enqueue a library call on the current stream of the tensors' device, whichever device is
     the current one."""
-    stream = ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
     if torch.cuda.current_device() == dev.index:
-        status = fn(*args, stream)
+        status = fn(block, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, stream)
+            status = fn(block, _raw_stream(dev.index))
     if status:
         _check(status)
 
@@ -788,70 +786,70 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, freq: torch.Tensor, *,
 
     inverse turns the other way: with the same arguments it is the gradient of this call.  Returns
     q_out, or (q_out, k_out); they may be q and k (in place)."""
-    lib = load()
-    B, H, n, D = _four(q, "q")
-    dev, dtype = q.device, q.dtype
-    code = _dtype_code(q)
-    qp, qs = _strided(q, dev, dtype, q.shape, "q")
+    lib = _lib or load()
+    B, H, n, D = shape = _four(q, "q")
+    dev, code = q.device, _dtype_code(q)
+    qa = _rows(q, q, shape, "q")
     R = 2 * freq.numel()
-    fp = _small(freq, dev, torch.float64, (R // 2,), "freq")
-    a = RotaryArgs(B, n, H, 0, D, R, int(interleaved), int(inverse), 1, 0, 0, 0, 0, 0, 0, scale)
-    pos = positions
+    fp = _small(freq, _cuda(dev), torch.float64, (R // 2,), "freq")
+    pos, axes, add, pa, pb, pn = positions, 1, 0, 0, 0, 0
     if isinstance(start, torch.Tensor):
         if positions is not None:
             raise ValueError("give positions or a start tensor, not both")
         if start.shape != (B,):
             raise ValueError(f"start must have shape {(B,)}, got {tuple(start.shape)}")
-        pos, a.pos_batch, a.add_index = start, start.stride(0), 1
+        pos, pb, add, start = start, start.stride(0), 1, 0
     elif positions is None:
-        a.start, a.add_index = start, 1
+        add = 1
     else:
-        a.start = start
         st = positions.stride()
         if positions.shape == (B, n):
-            a.pos_batch, a.pos_token = st
+            pb, pn = st
         elif positions.dim() == 3 and positions.shape[1:] == (B, n):
-            a.axes, (a.pos_axis, a.pos_batch, a.pos_token) = positions.shape[0], st
+            axes, (pa, pb, pn) = positions.shape[0], st
         else:
             raise ValueError(f"positions must have shape {(B, n)} or (axes, {B}, {n}), got "
                              f"{tuple(positions.shape)}")
+    pp = pos64 = 0
     if pos is not None:
         if pos.device != dev:
             raise ValueError("all tensors must be on the same CUDA device")
         if pos.dtype not in (torch.int32, torch.int64):
             raise TypeError(f"positions must be int32 or int64, got {pos.dtype}")
-        a.pos64 = int(pos.dtype == torch.int64)
+        pos64, pp = int(pos.dtype == torch.int64), pos.data_ptr()
     ap = _small(axis, dev, torch.uint8, (R // 2,), "axis")
-    if q_out is None:
-        q_out = torch.empty_like(q)
-    qop, qos = _strided(q_out, dev, dtype, q.shape, "q_out")
-    kp = kop = None
-    ks = kos = Strides()
+    Hk, ka, ko = 0, _NO_ROWS, _NO_ROWS
     if k is not None:
-        _four(k, "k")
-        a.Hk = k.shape[1]
-        kp, ks = _strided(k, dev, dtype, (B, a.Hk, n, D), "k")
+        Hk = _four(k, "k")[1]
+        ka = _rows(k, q, (B, Hk, n, D), "k")
         if k_out is None:
             k_out = torch.empty_like(k)
-        kop, kos = _strided(k_out, dev, dtype, k.shape, "k_out")
-    _call(dev, lib.rehyat_rotary, a, code, qp, qs, kp, ks, fp, ap,
-          None if pos is None else pos.data_ptr(), qop, qos, kop, kos)
+        ko = _rows(k_out, q, k.shape, "k_out")
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    qo = _rows(q_out, q, shape, "q_out")
+    _call(dev, lib.rehyat_rotary, _ROTARY.pack(
+        B, n, H, Hk, D, R, interleaved, inverse, axes, pos64, add, code, pa, pb, pn, start, fp, ap,
+        pp, *qa, *ka, *qo, *ko, scale))
     return q_out if k is None else (q_out, k_out)
 
 
-def _decay_args(q, k, scale: float) -> DecayArgs:
+_NO_ROWS = (0, 0, 0, 0)
+
+
+def _decay_sizes(q, k):
     B, H, N, D = _four(q, "q")
     Hk = _four(k, "k")[1]
     if Hk < 1 or H % Hk:
         raise ValueError(f"k's {Hk} heads must divide q's {H}")
-    return DecayArgs(B, H, Hk, N, D, scale)
+    return B, H, Hk, N, D
 
 
-def decay_workspace_size(a: DecayArgs, dtype_code: int, backward: bool = False) -> int:
+@functools.lru_cache(maxsize=1024)
+def decay_workspace_size(B: int, H: int, Hk: int, N: int, D: int, backward: bool = False) -> int:
+    """Bytes of scratch that decay_forward (or decay_backward) needs for these sizes."""
     n = ctypes.c_size_t(0)
-    status = load().rehyat_decay_workspace_size(a, dtype_code, int(backward), ctypes.byref(n))
-    if status:
-        _check(status)
+    _check(load().rehyat_decay_workspace_size(B, H, Hk, N, D, int(backward), ctypes.byref(n)))
     return n.value
 
 
@@ -866,28 +864,26 @@ def decay_forward(q, k, v, log_decay, *, scale: float = 1.0, lengths: torch.Tens
     into any result, zero in the output).  state [B,H,D,D] fp32: from the rows before.
     final_state True: returns (out, the state after the last row [B,H,D,D] fp32), which
     `decay_step` or the next call goes on from; a tensor: written there (it may be `state`)."""
-    lib = load()
-    a = _decay_args(q, k, scale)
-    dev, dtype, code = q.device, q.dtype, _dtype_code(q)
-    kv = (a.B, a.Hk, a.N, a.D)
-    square = (a.B, a.H, a.D, a.D)
-    qa, ka, va = (_strided(q, dev, dtype, q.shape, "q"), _strided(k, dev, dtype, kv, "k"),
-                  _strided(v, dev, dtype, kv, "v"))
-    gp = _small(log_decay, dev, torch.float32, (a.H,), "log_decay")
-    lp = _small(lengths, dev, torch.int32, (a.B,), "lengths")
+    lib = _lib or load()
+    B, H, Hk, N, D = _decay_sizes(q, k)
+    dev, code = q.device, _dtype_code(q)
+    shape, kv, square = q.shape, (B, Hk, N, D), (B, H, D, D)
+    qa, ka, va = _rows(q, q, shape, "q"), _rows(k, q, kv, "k"), _rows(v, q, kv, "v")
+    gp = _small(log_decay, _cuda(dev), torch.float32, (H,), "log_decay")
+    lp = _small(lengths, dev, torch.int32, (B,), "lengths")
     sp = _small(state, dev, torch.float32, square, "state")
     if out is None:
         out = torch.empty_like(q)
-    oa = _strided(out, dev, dtype, q.shape, "out")
+    oa = _rows(out, q, shape, "out")
     last = None
     if isinstance(final_state, torch.Tensor):
         last = final_state
     elif final_state:
         last = torch.empty(square, dtype=torch.float32, device=dev)
     fp = _small(last, dev, torch.float32, square, "final_state")
-    ws = _scratch(decay_workspace_size(a, code), dev, workspace)
-    _call(dev, lib.rehyat_decay_forward, a, code, *qa, *ka, *va, gp, lp, sp, *oa, fp,
-          ws.data_ptr(), ws.numel())
+    ws = _scratch(decay_workspace_size(B, H, Hk, N, D), dev, workspace)
+    _call(dev, lib.rehyat_decay_forward, _DECAY_FORWARD.pack(
+        B, H, Hk, N, D, code, *qa, *ka, *va, *oa, gp, lp, sp, fp, ws.data_ptr(), ws.numel(), scale))
     return out if last is None else (out, last)
 
 
@@ -899,25 +895,24 @@ def decay_backward(q, k, v, log_decay, dout, *, scale: float = 1.0,
     [B,H,N,D], dk, dv [B,Hk,N,D] (the inputs' type; dk and dv summed over the query heads that share
     them; zero on padding) and, with `state`, dstate [B,H,D,D] fp32.  dout [B,H,N,D]; dfinal
     [B,H,D,D] fp32 or None (zero)."""
-    lib = load()
-    a = _decay_args(q, k, scale)
-    dev, dtype, code = q.device, q.dtype, _dtype_code(q)
-    kv = (a.B, a.Hk, a.N, a.D)
-    square = (a.B, a.H, a.D, a.D)
-    qa, ka, va, doa = (_strided(q, dev, dtype, q.shape, "q"), _strided(k, dev, dtype, kv, "k"),
-                       _strided(v, dev, dtype, kv, "v"),
-                       _strided(dout, dev, dtype, q.shape, "dout"))
-    gp = _small(log_decay, dev, torch.float32, (a.H,), "log_decay")
-    lp = _small(lengths, dev, torch.int32, (a.B,), "lengths")
+    lib = _lib or load()
+    B, H, Hk, N, D = _decay_sizes(q, k)
+    dev, code = q.device, _dtype_code(q)
+    shape, kv, square = q.shape, (B, Hk, N, D), (B, H, D, D)
+    qa, ka, va = _rows(q, q, shape, "q"), _rows(k, q, kv, "k"), _rows(v, q, kv, "v")
+    doa = _rows(dout, q, shape, "dout")
+    gp = _small(log_decay, _cuda(dev), torch.float32, (H,), "log_decay")
+    lp = _small(lengths, dev, torch.int32, (B,), "lengths")
     sp = _small(state, dev, torch.float32, square, "state")
     fp = _small(dfinal, dev, torch.float32, square, "dfinal")
     g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v)}
     if state is not None:
         g["dstate"] = torch.empty(square, dtype=torch.float32, device=dev)
-    outs = [x for n in ("dq", "dk", "dv") for x in _strided(g[n], dev, dtype, g[n].shape, n)]
-    ws = _scratch(decay_workspace_size(a, code, True), dev, workspace)
-    _call(dev, lib.rehyat_decay_backward, a, code, *qa, *ka, *va, gp, lp, sp, *doa, fp, *outs,
-          g["dstate"].data_ptr() if state is not None else None, ws.data_ptr(), ws.numel())
+    ws = _scratch(decay_workspace_size(B, H, Hk, N, D, True), dev, workspace)
+    _call(dev, lib.rehyat_decay_backward, _DECAY_BACKWARD.pack(
+        B, H, Hk, N, D, code, *qa, *ka, *va, *doa, *_rows(g["dq"], q, shape, "dq"),
+        *_rows(g["dk"], q, kv, "dk"), *_rows(g["dv"], q, kv, "dv"), gp, lp, sp, fp,
+        g["dstate"].data_ptr() if state is not None else 0, ws.data_ptr(), ws.numel(), scale))
     return g
 
 
@@ -928,20 +923,19 @@ def decay_step(q, k, v, log_decay, state, *, scale: float = 1.0,
     is state[slots[b]] (without slots: state[b], pool = B); a negative slot is an idle entry (zero
     output, no state touched); a slot listed several times takes its tokens in batch order; one past
     the pool gives zeros and is reported by `sync_status`."""
-    lib = load()
-    a = _decay_args(q, k, scale)
-    if a.N != 1:
-        raise ValueError(f"a step takes one token of each sequence, got {a.N}")
-    dev, dtype, code = q.device, q.dtype, _dtype_code(q)
-    kv = (a.B, a.Hk, 1, a.D)
-    pool = state.shape[0] if slots is not None and state.dim() == 4 else a.B
-    qa, ka, va = (_strided(q, dev, dtype, q.shape, "q"), _strided(k, dev, dtype, kv, "k"),
-                  _strided(v, dev, dtype, kv, "v"))
-    gp = _small(log_decay, dev, torch.float32, (a.H,), "log_decay")
-    sp = _small(state, dev, torch.float32, (pool, a.H, a.D, a.D), "state")
-    lp = _small(slots, dev, torch.int32, (a.B,), "slots")
+    lib = _lib or load()
+    B, H, Hk, N, D = _decay_sizes(q, k)
+    if N != 1:
+        raise ValueError(f"a step takes one token of each sequence, got {N}")
+    dev, code = q.device, _dtype_code(q)
+    shape, kv = q.shape, (B, Hk, 1, D)
+    pool = state.shape[0] if slots is not None and state.dim() == 4 else B
+    qa, ka, va = _rows(q, q, shape, "q"), _rows(k, q, kv, "k"), _rows(v, q, kv, "v")
+    gp = _small(log_decay, _cuda(dev), torch.float32, (H,), "log_decay")
+    sp = _small(state, dev, torch.float32, (pool, H, D, D), "state")
+    lp = _small(slots, dev, torch.int32, (B,), "slots")
     if out is None:
         out = torch.empty_like(q)
-    oa = _strided(out, dev, dtype, q.shape, "out")
-    _call(dev, lib.rehyat_decay_step, a, code, *qa, *ka, *va, gp, sp, pool, lp, *oa)
+    _call(dev, lib.rehyat_decay_step, _DECAY_STEP.pack(
+        B, H, Hk, D, pool, code, *qa, *ka, *va, *_rows(out, q, shape, "out"), gp, sp, lp, scale))
     return out

@@ -75,33 +75,48 @@ __device__ __forceinline__ void turn(const Params& p, int pair, int b, int i, fl
   s *= p.scale * p.sign;
 }
 
+// Eight values of a row, as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]);
+struct Eight {
+  uint4 u[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = u[i];
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const;
+  __device__ __forceinline__ void set(const float (&v)[8]);
+};
 template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+__device__ __forceinline__ void Eight<float>::get(float (&v)[8]) const {
+  const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
 }
 template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void Eight<float>::set(const float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    u[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                      __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+}
+template <>
+__device__ __forceinline__ void Eight<__nv_bfloat16>::get(float (&v)[8]) const {
+  const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+template <>
+__device__ __forceinline__ void Eight<__nv_bfloat16>::set(const float (&v)[8]) {
   using sm100::pack_bf16x2;
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                            pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  u[0] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
 }
 
 // Heads [h0, h1) of the two tensors counted one after the other.
@@ -126,38 +141,52 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const Params p) {
   const int d1 = turns && !kInterleaved ? d0 + p.R / 2 : d0 + 8;
   const int h0 = blockIdx.y * p.heads_per_block;
   const int h1 = min(h0 + p.heads_per_block, p.t[0].heads + p.t[1].heads);
-#pragma unroll 2
-  for (int hh = h0; hh < h1; ++hh) {
-    const int w = hh >= p.t[0].heads;
-    const Tensor& t = p.t[w];
-    const int h = hh - (w ? p.t[0].heads : 0);
-    const T* x = static_cast<const T*>(t.x) + b * t.xb + h * t.xh + i * t.xn;
-    T* y = static_cast<T*>(t.y) + b * t.yb + h * t.yh + i * t.yn;
-    float v0[8], v1[8], o0[8], o1[8];
-    load8<T>(x + d0, v0);
-    load8<T>(x + d1, v1);
-    if (!turns) {
-      store8(y + d0, v0);
-      store8(y + d1, v1);
-      continue;
-    }
-    if (kInterleaved) {
+  // a batch of heads is loaded before any is stored (the output may be the input, so the compiler
+  // would not move a load past a store): eight 16-byte loads of a thread in flight
+  constexpr int kBatch = 8 / (int)sizeof(T);
+  for (int hb = h0; hb < h1; hb += kBatch) {
+    Eight<T> a[kBatch], z[kBatch];
+    T* y[kBatch];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        o0[2 * k] = v0[2 * k] * c[k] - v0[2 * k + 1] * s[k];
-        o0[2 * k + 1] = v0[2 * k + 1] * c[k] + v0[2 * k] * s[k];
-        o1[2 * k] = v1[2 * k] * c[4 + k] - v1[2 * k + 1] * s[4 + k];
-        o1[2 * k + 1] = v1[2 * k + 1] * c[4 + k] + v1[2 * k] * s[4 + k];
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        o0[k] = v0[k] * c[k] - v1[k] * s[k];
-        o1[k] = v1[k] * c[k] + v0[k] * s[k];
+    for (int m = 0; m < kBatch; ++m) {
+      const int hh = hb + m, w = hh >= p.t[0].heads;
+      const Tensor& t = p.t[w];
+      const int h = hh - (w ? p.t[0].heads : 0);
+      y[m] = static_cast<T*>(t.y) + b * t.yb + h * t.yh + i * t.yn;
+      if (hh < h1) {
+        const T* x = static_cast<const T*>(t.x) + b * t.xb + h * t.xh + i * t.xn;
+        a[m].load(x + d0);
+        z[m].load(x + d1);
       }
     }
-    store8(y + d0, o0);
-    store8(y + d1, o1);
+#pragma unroll
+    for (int m = 0; m < kBatch; ++m) {
+      if (hb + m >= h1) break;
+      if (turns) {
+        float v0[8], v1[8], o0[8], o1[8];
+        a[m].get(v0);
+        z[m].get(v1);
+        if (kInterleaved) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            o0[2 * k] = v0[2 * k] * c[k] - v0[2 * k + 1] * s[k];
+            o0[2 * k + 1] = v0[2 * k + 1] * c[k] + v0[2 * k] * s[k];
+            o1[2 * k] = v1[2 * k] * c[4 + k] - v1[2 * k + 1] * s[4 + k];
+            o1[2 * k + 1] = v1[2 * k + 1] * c[4 + k] + v1[2 * k] * s[4 + k];
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            o0[k] = v0[k] * c[k] - v1[k] * s[k];
+            o1[k] = v1[k] * c[k] + v0[k] * s[k];
+          }
+        }
+        a[m].set(o0);
+        z[m].set(o1);
+      }
+      a[m].store(y[m] + d0);
+      z[m].store(y[m] + d1);
+    }
   }
 }
 

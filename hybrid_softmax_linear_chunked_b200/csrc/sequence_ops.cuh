@@ -12,9 +12,15 @@ namespace {
 using rehyat::decay::Pass;
 using rehyat::decay::Rows;
 
-// log_decay, lengths and states are read in place by kernels that index them from these sizes.
-int check_decay(const rehyat_decay_args& a, rehyat_dtype dt) {
-  if (dt != REHYAT_F32 && dt != REHYAT_BF16) return fail(REHYAT_ERR_DTYPE, "unknown dtype %d", (int)dt);
+struct DecayDims {
+  int B, H, Hk, N, D;
+  rehyat_dtype dt;
+  float scale;
+};
+
+int check_decay(const DecayDims& a) {
+  if (a.dt != REHYAT_F32 && a.dt != REHYAT_BF16)
+    return fail(REHYAT_ERR_DTYPE, "unknown dtype %d", (int)a.dt);
   if (a.B < 1 || a.H < 1 || a.Hk < 1 || a.N < 0 || a.D < 1)
     return fail(REHYAT_ERR_ARG, "need B, H, Hk, D >= 1 and N >= 0 (B=%d H=%d Hk=%d N=%d D=%d)", a.B,
                 a.H, a.Hk, a.N, a.D);
@@ -30,14 +36,13 @@ int check_decay(const rehyat_decay_args& a, rehyat_dtype dt) {
 }
 
 // A strided [B, heads, N, D] tensor: aligned, whole 16-byte strides, rows that do not overlap.
-int check_rows(const char* what, const void* p, const rehyat_strides& s, int B, int heads, int N,
-               int D, rehyat_dtype dt) {
-  const int el = dt == REHYAT_BF16 ? 2 : 4;
-  if (N == 0) return REHYAT_OK;
-  if (!p) return fail(REHYAT_ERR_ARG, "null pointer (%s)", what);
-  if (!aligned16(p)) return fail(REHYAT_ERR_ALIGN, "%s is not 16-byte aligned", what);
+int check_rows(const char* what, const rehyat_rows& s, const DecayDims& a, int heads) {
+  const int el = a.dt == REHYAT_BF16 ? 2 : 4, D = a.D;
+  if (a.N == 0) return REHYAT_OK;
+  if (!s.p) return fail(REHYAT_ERR_ARG, "null pointer (%s)", what);
+  if (!aligned16(s.p)) return fail(REHYAT_ERR_ALIGN, "%s is not 16-byte aligned", what);
   const long long st[3] = {s.batch, s.head, s.row};
-  const int size[3] = {B, heads, N};
+  const int size[3] = {a.B, heads, a.N};
   for (int i = 0; i < 3; ++i) {
     if (size[i] == 1) continue;
     if (st[i] < D)
@@ -50,8 +55,8 @@ int check_rows(const char* what, const void* p, const rehyat_strides& s, int B, 
   return REHYAT_OK;
 }
 
-Rows rows_of(const void* p, const rehyat_strides& s, int group) {
-  return Rows{p, s.batch, s.head, s.row, group};
+Rows rows_of(const rehyat_rows& s, int group) {
+  return Rows{s.p, s.batch, s.head, s.row, group};
 }
 
 // Segments of a sequence: one CTA each, so their number trades whole waves of the 148 SMs against
@@ -82,7 +87,7 @@ struct DecayPlan {
   Segments seg;
   size_t fwd, bwd, part, total;
 };
-DecayPlan plan_decay(const rehyat_decay_args& a, bool backward) {
+DecayPlan plan_decay(const DecayDims& a, bool backward) {
   DecayPlan p{};
   const size_t BH = (size_t)a.B * a.H;
   p.seg = decay_segments((int)BH, a.N, true);
@@ -100,26 +105,25 @@ DecayPlan plan_decay(const rehyat_decay_args& a, bool backward) {
 
 // bf16 [B, heads, N, D] tensor with strides in elements, loaded and stored as 128-row x 64-column
 // boxes with 128-byte swizzle; columns past D read zeros and are not written.
-int make_map_rows(CUtensorMap* m, const void* base, const rehyat_strides& s, int D, int N,
-                  int heads, int B) {
+int make_map_rows(CUtensorMap* m, const Rows& s, int D, int N, int heads, int B) {
   EncodeTiledFn enc;
   RH_TRY(get_encoder(&enc));
   cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)heads, (cuuint64_t)B};
   // the stride of a single row, head or sequence is never used; any legal one will do
   const long long one = D;
-  cuuint64_t strides[3] = {(cuuint64_t)(N > 1 ? s.row : one) * 2,
-                           (cuuint64_t)(heads > 1 ? s.head : one) * 2,
-                           (cuuint64_t)(B > 1 ? s.batch : one) * 2};
+  cuuint64_t strides[3] = {(cuuint64_t)(N > 1 ? s.sn : one) * 2,
+                           (cuuint64_t)(heads > 1 ? s.sh : one) * 2,
+                           (cuuint64_t)(B > 1 ? s.sb : one) * 2};
   cuuint32_t box[4] = {64, 128, 1, 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
-                   box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(s.p), dims,
+                   strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(REHYAT_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return REHYAT_OK;
 }
 int map_of(CUtensorMap* m, const Rows& t, const Pass& p) {
-  return make_map_rows(m, t.p, rehyat_strides{t.sb, t.sh, t.sn}, p.D, p.N, p.H / t.group, p.B);
+  return make_map_rows(m, t, p.D, p.N, p.H / t.group, p.B);
 }
 
 // A launch behind another of the same call: with `behind`, it may start while that one still runs
@@ -180,7 +184,7 @@ int launch_decay_rows(const Pass& p, rehyat_dtype dt, bool out_f32, bool behind_
   RH_TRY(map_of(&mb, p.b, p));
   RH_TRY(map_of(&mc, p.c, p));
   mo = ma;  // unused with fp32 output
-  if (!out_f32) RH_TRY(make_map_rows(&mo, p.out, rehyat_strides{p.ob, p.oh, p.on}, p.D, p.N, p.H, p.B));
+  if (!out_f32) RH_TRY(make_map_rows(&mo, Rows{p.out, p.ob, p.oh, p.on, 1}, p.D, p.N, p.H, p.B));
   auto k = p.reverse ? (out_f32 ? decay_rows_bf16_kernel<true, true> : decay_rows_bf16_kernel<true, false>)
                      : decay_rows_bf16_kernel<false, false>;
   RH_TRY(cuda_check(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRwSmem),
@@ -222,7 +226,7 @@ int decay_prefix(Pass p, rehyat_dtype dt, const float* S0, float* last, const fl
   return REHYAT_OK;
 }
 
-Pass decay_pass(const rehyat_decay_args& a, const float* log_decay, const int* lengths,
+Pass decay_pass(const DecayDims& a, const float* log_decay, const int* lengths,
                 const Segments& s) {
   Pass p{};
   p.log_decay = log_decay;
@@ -234,8 +238,20 @@ Pass decay_pass(const rehyat_decay_args& a, const float* log_decay, const int* l
   return p;
 }
 
+void set_out(Pass& p, const rehyat_rows& o) {
+  p.out = o.p;
+  p.ob = o.batch; p.oh = o.head; p.on = o.row;
+}
+
 int check_states(const char* what, const float* S) {
   if (S && !aligned16(S)) return fail(REHYAT_ERR_ALIGN, "%s is not 16-byte aligned", what);
+  return REHYAT_OK;
+}
+
+int check_scratch(const DecayPlan& pl, const void* workspace, size_t ws_bytes) {
+  if (!workspace || ws_bytes < pl.total)
+    return fail(REHYAT_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", pl.total, ws_bytes);
+  if (!aligned16(workspace)) return fail(REHYAT_ERR_ALIGN, "workspace is not 16-byte aligned");
   return REHYAT_OK;
 }
 
@@ -243,12 +259,17 @@ int check_states(const char* what, const float* S) {
 
 extern "C" {
 
-int rehyat_rotary(rehyat_rotary_args a, rehyat_dtype dt, const void* q, rehyat_strides sq,
-                  const void* k, rehyat_strides sk, const double* freq, const unsigned char* axis,
-                  const void* pos, void* q_out, rehyat_strides sqo, void* k_out,
-                  rehyat_strides sko, void* stream) {
+// The binding packs these blocks by their layout.
+static_assert(sizeof(rehyat_rotary_args) == 240 && sizeof(rehyat_decay_forward_args) == 208 &&
+                  sizeof(rehyat_decay_backward_args) == 312 && sizeof(rehyat_decay_step_args) == 184,
+              "argument block layout");
+
+int rehyat_rotary(const rehyat_rotary_args* args, void* stream) {
   g_msg[0] = 0;
-  if (dt != REHYAT_F32 && dt != REHYAT_BF16) return fail(REHYAT_ERR_DTYPE, "unknown dtype %d", (int)dt);
+  if (!args) return fail(REHYAT_ERR_ARG, "null pointer (args)");
+  const rehyat_rotary_args& a = *args;
+  if (a.dtype != REHYAT_F32 && a.dtype != REHYAT_BF16)
+    return fail(REHYAT_ERR_DTYPE, "unknown dtype %d", a.dtype);
   if (a.B < 1 || a.n < 0 || a.Hq < 1 || a.Hk < 0 || a.D < 1)
     return fail(REHYAT_ERR_ARG, "need B, Hq, D >= 1 and n, Hk >= 0 (B=%d n=%d Hq=%d Hk=%d D=%d)", a.B,
                 a.n, a.Hq, a.Hk, a.D);
@@ -258,13 +279,16 @@ int rehyat_rotary(rehyat_rotary_args a, rehyat_dtype dt, const void* q, rehyat_s
     return fail(REHYAT_ERR_ARG, "axes=%d outside 1 .. %d", a.axes, rehyat::rotary::kMaxAxes);
   if (!std::isfinite(a.scale)) return fail(REHYAT_ERR_ARG, "scale must be finite");
   if (a.n == 0) return REHYAT_OK;
-  if (!q || !q_out || !freq || (a.Hk > 0 && (!k || !k_out)))
+  if (!a.q.p || !a.q_out.p || !a.freq || (a.Hk > 0 && (!a.k.p || !a.k_out.p)))
     return fail(REHYAT_ERR_ARG, "null pointer");
-  const bool bf16 = dt == REHYAT_BF16;
+  const bool bf16 = a.dtype == REHYAT_BF16;
   const int el = bf16 ? 2 : 4;
   rehyat::rotary::Params p{};
-  p.t[0] = {q, q_out, sq.batch, sq.head, sq.row, sqo.batch, sqo.head, sqo.row, a.Hq};
-  p.t[1] = {k, k_out, sk.batch, sk.head, sk.row, sko.batch, sko.head, sko.row, a.Hk};
+  auto tensor = [](const rehyat_rows& x, const rehyat_rows& y, int heads) {
+    return rehyat::rotary::Tensor{x.p, y.p, x.batch, x.head, x.row, y.batch, y.head, y.row, heads};
+  };
+  p.t[0] = tensor(a.q, a.q_out, a.Hq);
+  p.t[1] = tensor(a.k, a.k_out, a.Hk);
   bool whole = a.R % 16 == 0 && a.D % 16 == 0, in_place = true;
   for (int i = 0; i < (a.Hk ? 2 : 1); ++i) {
     const rehyat::rotary::Tensor& t = p.t[i];
@@ -279,7 +303,7 @@ int rehyat_rotary(rehyat_rotary_args a, rehyat_dtype dt, const void* q, rehyat_s
   }
   p.B = a.B; p.n = a.n; p.D = a.D; p.R = a.R;
   p.interleaved = a.interleaved; p.copy_tail = !in_place && a.R < a.D;
-  p.freq = freq; p.axis = axis; p.pos = pos; p.pos64 = a.pos64; p.axes = a.axes;
+  p.freq = a.freq; p.axis = a.axis; p.pos = a.pos; p.pos64 = a.pos64; p.axes = a.axes;
   p.pa = a.pos_axis; p.pb = a.pos_batch; p.pn = a.pos_token;
   p.add_index = a.add_index; p.start = a.start;
   p.scale = a.scale; p.sign = a.inverse ? -1.f : 1.f;
@@ -309,108 +333,98 @@ int rehyat_rotary(rehyat_rotary_args a, rehyat_dtype dt, const void* q, rehyat_s
   return cuda_check(cudaGetLastError(), "rotary launch");
 }
 
-int rehyat_decay_workspace_size(rehyat_decay_args a, rehyat_dtype dt, int backward,
-                                size_t* bytes) {
+int rehyat_decay_workspace_size(int B, int H, int Hk, int N, int D, int backward, size_t* bytes) {
   g_msg[0] = 0;
-  RH_TRY(check_decay(a, dt));
+  const DecayDims d{B, H, Hk, N, D, REHYAT_BF16, 1.f};
+  RH_TRY(check_decay(d));
   if (!bytes) return fail(REHYAT_ERR_ARG, "null pointer");
-  *bytes = plan_decay(a, backward != 0).total;
+  *bytes = plan_decay(d, backward != 0).total;
   return REHYAT_OK;
 }
 
-int rehyat_decay_forward(rehyat_decay_args a, rehyat_dtype dt, const void* q, rehyat_strides sq,
-                         const void* k, rehyat_strides sk, const void* v, rehyat_strides sv,
-                         const float* log_decay, const int* lengths, const float* S0, void* out,
-                         rehyat_strides so, float* S_last, void* workspace, size_t ws_bytes,
-                         void* stream) {
+int rehyat_decay_forward(const rehyat_decay_forward_args* args, void* stream) {
   g_msg[0] = 0;
-  RH_TRY(check_decay(a, dt));
-  if (!log_decay) return fail(REHYAT_ERR_ARG, "null pointer (log_decay)");
-  RH_TRY(check_rows("q", q, sq, a.B, a.H, a.N, a.D, dt));
-  RH_TRY(check_rows("k", k, sk, a.B, a.Hk, a.N, a.D, dt));
-  RH_TRY(check_rows("v", v, sv, a.B, a.Hk, a.N, a.D, dt));
-  RH_TRY(check_rows("out", out, so, a.B, a.H, a.N, a.D, dt));
-  RH_TRY(check_states("S0", S0));
-  RH_TRY(check_states("S_last", S_last));
-  const DecayPlan pl = plan_decay(a, false);
-  if (!workspace || ws_bytes < pl.total)
-    return fail(REHYAT_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", pl.total, ws_bytes);
-  if (!aligned16(workspace)) return fail(REHYAT_ERR_ALIGN, "workspace is not 16-byte aligned");
+  if (!args) return fail(REHYAT_ERR_ARG, "null pointer (args)");
+  const rehyat_decay_forward_args& a = *args;
+  const DecayDims d{a.B, a.H, a.Hk, a.N, a.D, (rehyat_dtype)a.dtype, a.scale};
+  RH_TRY(check_decay(d));
+  if (!a.log_decay) return fail(REHYAT_ERR_ARG, "null pointer (log_decay)");
+  RH_TRY(check_rows("q", a.q, d, a.H));
+  RH_TRY(check_rows("k", a.k, d, a.Hk));
+  RH_TRY(check_rows("v", a.v, d, a.Hk));
+  RH_TRY(check_rows("out", a.out, d, a.H));
+  RH_TRY(check_states("S0", a.S0));
+  RH_TRY(check_states("S_last", a.S_last));
+  const DecayPlan pl = plan_decay(d, false);
+  RH_TRY(check_scratch(pl, a.workspace, a.ws_bytes));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int group = a.H / a.Hk;
-  Pass p = decay_pass(a, log_decay, lengths, pl.seg);
-  p.a = rows_of(q, sq, 1);
-  p.b = rows_of(k, sk, group);
-  p.c = rows_of(v, sv, group);
+  Pass p = decay_pass(d, a.log_decay, a.lengths, pl.seg);
+  p.a = rows_of(a.q, 1);
+  p.b = rows_of(a.k, group);
+  p.c = rows_of(a.v, group);
   p.e = 1;
   p.sp = p.si = a.scale;
-  p.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.fwd);
+  p.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + pl.fwd);
   bool scanned;
-  RH_TRY(decay_prefix(p, dt, S0, S_last, &p.prefix, &scanned, st));
+  RH_TRY(decay_prefix(p, d.dt, a.S0, a.S_last, &p.prefix, &scanned, st));
   if (a.N == 0) return REHYAT_OK;
-  p.out = out;
-  p.ob = so.batch; p.oh = so.head; p.on = so.row;
-  return launch_decay_rows(p, dt, false, scanned, st);
+  set_out(p, a.out);
+  return launch_decay_rows(p, d.dt, false, scanned, st);
 }
 
-int rehyat_decay_backward(rehyat_decay_args a, rehyat_dtype dt, const void* q, rehyat_strides sq,
-                          const void* k, rehyat_strides sk, const void* v, rehyat_strides sv,
-                          const float* log_decay, const int* lengths, const float* S0,
-                          const void* dout, rehyat_strides sdo, const float* dS_last, void* dq,
-                          rehyat_strides sdq, void* dk, rehyat_strides sdk, void* dv,
-                          rehyat_strides sdv, float* dS0, void* workspace, size_t ws_bytes,
-                          void* stream) {
+int rehyat_decay_backward(const rehyat_decay_backward_args* args, void* stream) {
   g_msg[0] = 0;
-  RH_TRY(check_decay(a, dt));
-  if (!log_decay) return fail(REHYAT_ERR_ARG, "null pointer (log_decay)");
-  RH_TRY(check_rows("q", q, sq, a.B, a.H, a.N, a.D, dt));
-  RH_TRY(check_rows("k", k, sk, a.B, a.Hk, a.N, a.D, dt));
-  RH_TRY(check_rows("v", v, sv, a.B, a.Hk, a.N, a.D, dt));
-  RH_TRY(check_rows("dout", dout, sdo, a.B, a.H, a.N, a.D, dt));
-  RH_TRY(check_rows("dq", dq, sdq, a.B, a.H, a.N, a.D, dt));
-  RH_TRY(check_rows("dk", dk, sdk, a.B, a.Hk, a.N, a.D, dt));
-  RH_TRY(check_rows("dv", dv, sdv, a.B, a.Hk, a.N, a.D, dt));
-  RH_TRY(check_states("S0", S0));
-  RH_TRY(check_states("dS_last", dS_last));
-  RH_TRY(check_states("dS0", dS0));
-  const DecayPlan pl = plan_decay(a, true);
-  if (!workspace || ws_bytes < pl.total)
-    return fail(REHYAT_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", pl.total, ws_bytes);
-  if (!aligned16(workspace)) return fail(REHYAT_ERR_ALIGN, "workspace is not 16-byte aligned");
+  if (!args) return fail(REHYAT_ERR_ARG, "null pointer (args)");
+  const rehyat_decay_backward_args& a = *args;
+  const DecayDims d{a.B, a.H, a.Hk, a.N, a.D, (rehyat_dtype)a.dtype, a.scale};
+  RH_TRY(check_decay(d));
+  if (!a.log_decay) return fail(REHYAT_ERR_ARG, "null pointer (log_decay)");
+  RH_TRY(check_rows("q", a.q, d, a.H));
+  RH_TRY(check_rows("k", a.k, d, a.Hk));
+  RH_TRY(check_rows("v", a.v, d, a.Hk));
+  RH_TRY(check_rows("dout", a.dout, d, a.H));
+  RH_TRY(check_rows("dq", a.dq, d, a.H));
+  RH_TRY(check_rows("dk", a.dk, d, a.Hk));
+  RH_TRY(check_rows("dv", a.dv, d, a.Hk));
+  RH_TRY(check_states("S0", a.S0));
+  RH_TRY(check_states("dS_last", a.dS_last));
+  RH_TRY(check_states("dS0", a.dS0));
+  const DecayPlan pl = plan_decay(d, true);
+  RH_TRY(check_scratch(pl, a.workspace, a.ws_bytes));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const int group = a.H / a.Hk;
-  const Rows rq = rows_of(q, sq, 1), rk = rows_of(k, sk, group), rv = rows_of(v, sv, group),
-             rdo = rows_of(dout, sdo, 1);
+  const Rows rq = rows_of(a.q, 1), rk = rows_of(a.k, group), rv = rows_of(a.v, group),
+             rdo = rows_of(a.dout, 1);
 
   // dQ: forward in time over the states of the prompt, transposed
-  Pass f = decay_pass(a, log_decay, lengths, pl.seg);
+  Pass f = decay_pass(d, a.log_decay, a.lengths, pl.seg);
   f.delta = reinterpret_cast<float*>(ws + pl.fwd);
   f.e = 1;
   bool scanned = false;
   if (a.N > 0) {
     f.b = rk;
     f.c = rv;
-    RH_TRY(decay_prefix(f, dt, S0, nullptr, &f.prefix, &scanned, st));
+    RH_TRY(decay_prefix(f, d.dt, a.S0, nullptr, &f.prefix, &scanned, st));
     f.a = rdo;
     f.b = rv;
     f.c = rk;
     f.transposed = 1;
     f.sp = f.si = a.scale;
-    f.out = dq;
-    f.ob = sdq.batch; f.oh = sdq.head; f.on = sdq.row;
-    RH_TRY(launch_decay_rows(f, dt, false, scanned, st));
+    set_out(f, a.dq);
+    RH_TRY(launch_decay_rows(f, d.dt, false, scanned, st));
   }
 
   // dK, dV: backward in time over the gradient of the state, sum of scale * q dO^T
-  Pass r = decay_pass(a, log_decay, lengths, pl.seg);
+  Pass r = decay_pass(d, a.log_decay, a.lengths, pl.seg);
   r.delta = reinterpret_cast<float*>(ws + pl.bwd);
   r.reverse = 1;
   r.e = 0;
   r.b = rq;
   r.c = rdo;
   r.sp = r.sd = a.scale;
-  RH_TRY(decay_prefix(r, dt, dS_last, dS0, &r.prefix, &scanned, st));
+  RH_TRY(decay_prefix(r, d.dt, a.dS_last, a.dS0, &r.prefix, &scanned, st));
   if (a.N == 0) return REHYAT_OK;
   float* part = reinterpret_cast<float*>(ws + pl.part);
   for (int i = 0; i < 2; ++i) {
@@ -419,59 +433,57 @@ int rehyat_decay_backward(rehyat_decay_args a, rehyat_dtype dt, const void* q, r
     p.b = i ? rq : rdo;
     p.c = i ? rdo : rq;
     p.transposed = i ? 0 : 1;
-    void* dst = i ? dv : dk;
-    const rehyat_strides& s = i ? sdv : sdk;
+    const rehyat_rows& dst = i ? a.dv : a.dk;
     if (group == 1) {
-      p.out = dst;
-      p.ob = s.batch; p.oh = s.head; p.on = s.row;
-      RH_TRY(launch_decay_rows(p, dt, false, scanned && i == 0, st));
+      set_out(p, dst);
+      RH_TRY(launch_decay_rows(p, d.dt, false, scanned && i == 0, st));
       continue;
     }
-    p.out = part;
-    p.on = a.D; p.oh = (long long)a.N * a.D; p.ob = p.oh * a.H;
-    RH_TRY(launch_decay_rows(p, dt, true, scanned && i == 0, st));
-    const long long vec = (long long)a.N * a.D / 4;
+    const long long head = (long long)a.N * a.D;
+    set_out(p, rehyat_rows{part, head * a.H, head, a.D});
+    RH_TRY(launch_decay_rows(p, d.dt, true, scanned && i == 0, st));
+    const long long vec = head / 4;
     const dim3 grid((unsigned)(vec / 1024 + 1 < 4096 ? vec / 1024 + 1 : 4096), a.B * a.Hk);
-    if (dt == REHYAT_BF16)
+    if (d.dt == REHYAT_BF16)
       rehyat::decay::decay_group_sum_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(
-          part, static_cast<__nv_bfloat16*>(dst), s.batch, s.head, s.row, a.Hk, group, a.N, a.D);
+          part, static_cast<__nv_bfloat16*>(dst.p), dst.batch, dst.head, dst.row, a.Hk, group, a.N,
+          a.D);
     else
       rehyat::decay::decay_group_sum_kernel<float><<<grid, 256, 0, st>>>(
-          part, static_cast<float*>(dst), s.batch, s.head, s.row, a.Hk, group, a.N, a.D);
+          part, static_cast<float*>(dst.p), dst.batch, dst.head, dst.row, a.Hk, group, a.N, a.D);
     RH_TRY(cuda_check(cudaGetLastError(), "decay group sum launch"));
   }
   return REHYAT_OK;
 }
 
-int rehyat_decay_step(rehyat_decay_args a, rehyat_dtype dt, const void* q, rehyat_strides sq,
-                      const void* k, rehyat_strides sk, const void* v, rehyat_strides sv,
-                      const float* log_decay, float* state, int pool, const int* slots, void* out,
-                      rehyat_strides so, void* stream) {
+int rehyat_decay_step(const rehyat_decay_step_args* args, void* stream) {
   g_msg[0] = 0;
-  a.N = 1;
-  RH_TRY(check_decay(a, dt));
-  if (!log_decay || !state) return fail(REHYAT_ERR_ARG, "null pointer");
-  RH_TRY(check_rows("q", q, sq, a.B, a.H, 1, a.D, dt));
-  RH_TRY(check_rows("k", k, sk, a.B, a.Hk, 1, a.D, dt));
-  RH_TRY(check_rows("v", v, sv, a.B, a.Hk, 1, a.D, dt));
-  RH_TRY(check_rows("out", out, so, a.B, a.H, 1, a.D, dt));
-  RH_TRY(check_states("state", state));
-  if (pool < 1 || (!slots && pool < a.B))
-    return fail(REHYAT_ERR_ARG, "a pool of %d states for %d sequences", pool, a.B);
+  if (!args) return fail(REHYAT_ERR_ARG, "null pointer (args)");
+  const rehyat_decay_step_args& a = *args;
+  const DecayDims d{a.B, a.H, a.Hk, 1, a.D, (rehyat_dtype)a.dtype, a.scale};
+  RH_TRY(check_decay(d));
+  if (!a.log_decay || !a.state) return fail(REHYAT_ERR_ARG, "null pointer");
+  RH_TRY(check_rows("q", a.q, d, a.H));
+  RH_TRY(check_rows("k", a.k, d, a.Hk));
+  RH_TRY(check_rows("v", a.v, d, a.Hk));
+  RH_TRY(check_rows("out", a.out, d, a.H));
+  RH_TRY(check_states("state", a.state));
+  if (a.pool < 1 || (!a.slots && a.pool < a.B))
+    return fail(REHYAT_ERR_ARG, "a pool of %d states for %d sequences", a.pool, a.B);
   rehyat::decay::StepParams p{};
   const int group = a.H / a.Hk;
-  p.q = rows_of(q, sq, 1);
-  p.k = rows_of(k, sk, group);
-  p.v = rows_of(v, sv, group);
-  p.out = out;
-  p.ob = so.batch; p.oh = so.head;
-  p.log_decay = log_decay; p.state = state; p.slots = slots;
-  p.B = a.B; p.H = a.H; p.D = a.D; p.pool = pool; p.scale = a.scale;
+  p.q = rows_of(a.q, 1);
+  p.k = rows_of(a.k, group);
+  p.v = rows_of(a.v, group);
+  p.out = a.out.p;
+  p.ob = a.out.batch; p.oh = a.out.head;
+  p.log_decay = a.log_decay; p.state = a.state; p.slots = a.slots;
+  p.B = a.B; p.H = a.H; p.D = a.D; p.pool = a.pool; p.scale = a.scale;
   using namespace rehyat::decay;
   const dim3 grid((a.D + kStepCols - 1) / kStepCols, a.H, a.B);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int passes = (a.D + 15) / 16;  // of 16 rows
-  const bool bf16 = dt == REHYAT_BF16;
+  const bool bf16 = d.dt == REHYAT_BF16;
   auto kern = passes <= 4 ? (bf16 ? decay_step_kernel<__nv_bfloat16, 4> : decay_step_kernel<float, 4>)
                           : (bf16 ? decay_step_kernel<__nv_bfloat16, 8> : decay_step_kernel<float, 8>);
   kern<<<grid, kStepThreads, 0, st>>>(p);

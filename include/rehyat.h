@@ -309,20 +309,22 @@ int rehyat_segment_attend(rehyat_dims d, rehyat_dtype dt, int T, int frame_token
  * Rotary positions for q and k, and linear attention with a decay per head: the pure recurrent
  * layer of a stack, as a chunked form for prompts, its gradients, and one token at a time.
  *
- * These calls take tensors by strides: rehyat_strides gives the elements between two sequences,
- * two heads and two rows of a [B, heads, N, D] tensor whose D elements are contiguous, so a
- * [B, N, heads, D] projection or a slice of a packed qkv is read in place.  Unless stated,
- * pointers and strides are multiples of 16 bytes (the stride of a dimension of size 1 is not
- * looked at), and a written tensor overlaps no other argument. */
+ * Each call takes one block of arguments, read before it returns.  Tensors of rows come with
+ * strides: rehyat_rows gives the elements between two sequences, two heads and two rows of a
+ * [B, heads, N, D] tensor whose D elements are contiguous, so a [B, N, heads, D] projection or a
+ * slice of a packed qkv is read in place.  Unless stated, pointers and strides are multiples of 16
+ * bytes (the stride of a dimension of size 1 is not looked at), and a written tensor overlaps no
+ * other argument.  `dtype` (a rehyat_dtype) is the type of all rows. */
 typedef struct {
+  void* p;
   long long batch, head, row;
-} rehyat_strides;
+} rehyat_rows;
 
 /* Rotary positions: pair p < R/2 of every head's first R dimensions turns by a = pos * freq[p],
  *   (x1, x2) -> scale * (x1 cos a - x2 sin a, x2 cos a + x1 sin a),
  * with (x1, x2) = (x[p], x[p + R/2]), or (x[2p], x[2p + 1]) when interleaved; dimensions R .. D-1
  * are copied.  inverse != 0 turns by -a: the gradient of the same call.  One launch turns q
- * [B,Hq,n,D] and k [B,Hk,n,D] (Hk = 0 and null k pointers: q alone).
+ * [B,Hq,n,D] and k [B,Hk,n,D] (Hk = 0: q alone).
  *   freq  [R/2] fp64, radians per position (a stretched context is a change of freq and scale);
  *   pos   the position of token i of sequence b on axis `axis[p]` (axis [R/2] bytes < axes, or NULL
  *         for axis 0), at pos[axis*pos_axis + b*pos_batch + i*pos_token] (int32, or int64 with
@@ -336,14 +338,15 @@ typedef struct {
   int interleaved, inverse;
   int axes;            /* 1..4 */
   int pos64, add_index;
-  long long pos_axis, pos_batch, pos_token;
-  long long start;
+  int dtype;
+  long long pos_axis, pos_batch, pos_token, start;
+  const double* freq;
+  const unsigned char* axis;
+  const void* pos;
+  rehyat_rows q, k, q_out, k_out;
   float scale;
 } rehyat_rotary_args;
-int rehyat_rotary(rehyat_rotary_args a, rehyat_dtype dt, const void* q, rehyat_strides sq,
-                  const void* k, rehyat_strides sk, const double* freq, const unsigned char* axis,
-                  const void* pos, void* q_out, rehyat_strides sqo, void* k_out,
-                  rehyat_strides sko, void* stream);
+int rehyat_rotary(const rehyat_rotary_args* args, void* stream);
 
 /* Linear attention with a decay L_h = exp(log_decay[h]) per head (log_decay [H] fp32, normally
  * <= 0; -inf forgets at once; a constant, not differentiated).  H query heads share Hk key/value
@@ -354,44 +357,59 @@ int rehyat_rotary(rehyat_rotary_args a, rehyat_dtype dt, const void* q, rehyat_s
  *   S_n = L^n S_0 + sum_{j<n} L^(n-1-j) k_j v_j^T
  * Rows n .. N-1 are padding: never read into a result, and zero in every output.
  * D a multiple of 8 up to 128; N may be 0.  bf16: tensor-core products with fp32 accumulation
- * (the states are summed from two-part products, to fp32 accuracy).  fp32: CUDA cores. */
+ * (the states are summed from two-part products, to fp32 accuracy).  fp32: CUDA cores.
+ * rehyat_decay_workspace_size: device scratch that the forward (backward = 0) or the gradients
+ * need for these sizes. */
+int rehyat_decay_workspace_size(int B, int H, int Hk, int N, int D, int backward, size_t* bytes);
+
+/* q, out [B,H,N,D]; k, v [B,Hk,N,D]; S0 [B,H,D,D] fp32 or NULL (zero); S_last [B,H,D,D] fp32 or
+ * NULL, written with S_n (it may be S0). */
 typedef struct {
-  int B, H, Hk, N, D;
+  int B, H, Hk, N, D, dtype;
+  rehyat_rows q, k, v, out;
+  const float* log_decay;
+  const int* lengths;
+  const float* S0;
+  float* S_last;
+  void* workspace;
+  size_t ws_bytes;
   float scale;
-} rehyat_decay_args;
-int rehyat_decay_workspace_size(rehyat_decay_args a, rehyat_dtype dt, int backward,
-                                size_t* bytes);
+} rehyat_decay_forward_args;
+int rehyat_decay_forward(const rehyat_decay_forward_args* args, void* stream);
 
-/* q [B,H,N,D], k, v [B,Hk,N,D], out [B,H,N,D] (dtype); S0 [B,H,D,D] fp32 or NULL (zero); S_last
- * [B,H,D,D] fp32 or NULL, written with S_n (it may be S0). */
-int rehyat_decay_forward(rehyat_decay_args a, rehyat_dtype dt, const void* q, rehyat_strides sq,
-                         const void* k, rehyat_strides sk, const void* v, rehyat_strides sv,
-                         const float* log_decay, const int* lengths, const float* S0, void* out,
-                         rehyat_strides so, float* S_last, void* workspace, size_t ws_bytes,
-                         void* stream);
+/* Gradients of sum(dout * out) + sum(dS_last * S_n): dq [B,H,N,D], dk, dv [B,Hk,N,D] (dk and dv
+ * summed over the query heads that share them) and, unless NULL, dS0 [B,H,D,D] fp32.  dout
+ * [B,H,N,D]; dS_last [B,H,D,D] fp32 or NULL (zero). */
+typedef struct {
+  int B, H, Hk, N, D, dtype;
+  rehyat_rows q, k, v, dout, dq, dk, dv;
+  const float* log_decay;
+  const int* lengths;
+  const float* S0;
+  const float* dS_last;
+  float* dS0;
+  void* workspace;
+  size_t ws_bytes;
+  float scale;
+} rehyat_decay_backward_args;
+int rehyat_decay_backward(const rehyat_decay_backward_args* args, void* stream);
 
-/* Gradients of sum(dout * out) + sum(dS_last * S_n): dq [B,H,N,D], dk, dv [B,Hk,N,D] (dtype; dk
- * and dv summed over the query heads that share them) and, unless NULL, dS0 [B,H,D,D] fp32.
- * dS_last NULL: zero. */
-int rehyat_decay_backward(rehyat_decay_args a, rehyat_dtype dt, const void* q, rehyat_strides sq,
-                          const void* k, rehyat_strides sk, const void* v, rehyat_strides sv,
-                          const float* log_decay, const int* lengths, const float* S0,
-                          const void* dout, rehyat_strides sdo, const float* dS_last, void* dq,
-                          rehyat_strides sdq, void* dk, rehyat_strides sdk, void* dv,
-                          rehyat_strides sdv, float* dS0, void* workspace, size_t ws_bytes,
-                          void* stream);
-
-/* One token of every sequence (a.N is not looked at; the row strides neither):
+/* One token of every sequence (rows of N = 1; row strides are not looked at):
  *   S <- L S + k v^T,  o = scale * q S        state [pool,H,D,D] fp32, in place;
  * sequence b's state is state[slots[b]] (slots [B] int32 on the device; NULL: state[b], pool >= B).
  * A negative slot is an idle entry: its output is zero and no state is touched.  A slot that
  * stands several times in `slots` takes those tokens in batch order, each reading the state the
  * one before left.  A slot >= pool is not touched, gives zeros, and the next rehyat_sync_status()
  * returns REHYAT_ERR_BOUNDS. */
-int rehyat_decay_step(rehyat_decay_args a, rehyat_dtype dt, const void* q, rehyat_strides sq,
-                      const void* k, rehyat_strides sk, const void* v, rehyat_strides sv,
-                      const float* log_decay, float* state, int pool, const int* slots, void* out,
-                      rehyat_strides so, void* stream);
+typedef struct {
+  int B, H, Hk, D, pool, dtype;
+  rehyat_rows q, k, v, out;
+  const float* log_decay;
+  float* state;
+  const int* slots;
+  float scale;
+} rehyat_decay_step_args;
+int rehyat_decay_step(const rehyat_decay_step_args* args, void* stream);
 
 /* Failure-path self test (no counterpart on the pages): enqueue on `stream` one small kernel whose
  * warps wait on an mbarrier that nothing arrives on, with the same bounded wait the other

@@ -291,7 +291,7 @@ def test_calls_repeat_bit_for_bit_and_replay_from_graphs(dev):
     p = problem(dev, torch.bfloat16, 2, 4, 2, 700, 128, True, seed=17)
     lengths = torch.tensor([700, 333], dtype=torch.int32, device=dev)
     S = p["S0"].clone()
-    size = rb.decay_workspace_size(rb.DecayArgs(2, 4, 2, 700, 128, 0.1), rb.REHYAT_BF16, True)
+    size = rb.decay_workspace_size(2, 4, 2, 700, 128, True)
     ws = torch.empty(size, dtype=torch.uint8, device=dev)  # shared by every call below
 
     def step():

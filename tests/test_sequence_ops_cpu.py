@@ -20,40 +20,36 @@ def lib():
     return rb.load()
 
 
-def st(heads, n=N, d=D):
-    return rb.Strides(heads * n * d, n * d, d)
+def rows(heads, p=FAKE, n=N, d=D):
+    return (p, heads * n * d, n * d, d)
 
 
-def decay(lib, call="forward", dt=rb.REHYAT_BF16, ws_bytes=1 << 40, ws=FAKE, **kw):
-    a = dict(B=B, H=H, Hk=HK, N=N, D=D, scale=1.0)
-    ptr = dict(q=FAKE, k=FAKE, v=FAKE, out=FAKE, g=FAKE, S0=None, last=FAKE, dout=FAKE, dq=FAKE,
-               dk=FAKE, dv=FAKE, state=FAKE, slots=None, pool=B)
-    sq, sk = kw.pop("sq", st(H)), kw.pop("sk", st(HK))
-    a.update({n: kw.pop(n) for n in list(kw) if n in a})
-    ptr.update(kw)
-    args = rb.DecayArgs(*a.values())
-    rows = (ptr["q"], sq, ptr["k"], sk, ptr["v"], st(HK))
-    if call == "forward":
-        return lib.rehyat_decay_forward(args, dt, *rows, ptr["g"], None, ptr["S0"], ptr["out"],
-                                        st(H), ptr["last"], ws, ws_bytes, None)
-    if call == "backward":
-        return lib.rehyat_decay_backward(args, dt, *rows, ptr["g"], None, ptr["S0"], ptr["dout"],
-                                         st(H), None, ptr["dq"], st(H), ptr["dk"], st(HK),
-                                         ptr["dv"], st(HK), None, ws, ws_bytes, None)
-    return lib.rehyat_decay_step(args, dt, *rows, ptr["g"], ptr["state"], ptr["pool"],
-                                 ptr["slots"], ptr["out"], st(H), None)
+def decay(lib, call="forward", **kw):
+    a = dict(B=B, H=H, Hk=HK, N=N, D=D, pool=B, dtype=rb.REHYAT_BF16, q=rows(H), k=rows(HK),
+             v=rows(HK), out=rows(H), dout=rows(H), dq=rows(H), dk=rows(HK), dv=rows(HK), g=FAKE,
+             lengths=0, S0=0, last=FAKE, dlast=0, dS0=0, state=FAKE, slots=0, ws=FAKE,
+             ws_bytes=1 << 40, scale=1.0)
+    a.update(kw)
+    order = {"forward": "B H Hk N D dtype q k v out g lengths S0 last ws ws_bytes scale",
+             "backward": "B H Hk N D dtype q k v dout dq dk dv g lengths S0 dlast dS0 ws ws_bytes "
+                         "scale",
+             "step": "B H Hk D pool dtype q k v out g state slots scale"}[call].split()
+    flat = [y for n in order for y in (a[n] if isinstance(a[n], tuple) else (a[n],))]
+    return getattr(lib, "rehyat_decay_" + call)(
+        getattr(rb, "_DECAY_" + call.upper()).pack(*flat), None)
 
 
 @pytest.mark.parametrize("kw,status", [
     (dict(B=0), -1), (dict(Hk=3), -1), (dict(Hk=0), -1), (dict(N=-1), -1), (dict(D=0), -1),
     (dict(D=60), -2), (dict(D=136), -2), (dict(B=70000), -2), (dict(H=40000, Hk=40000), -2),
-    (dict(scale=math.nan), -1), (dict(scale=math.inf), -1), (dict(dt=7), -3),
-    (dict(q=None), -1), (dict(v=FAKE + 8), -7), (dict(g=None), -1), (dict(S0=FAKE + 4), -7),
-    (dict(sq=rb.Strides(H * N * D, N * D, D - 8)), -1),     # rows overlap
-    (dict(sk=rb.Strides(HK * N * D, 0, D)), -1),            # heads expanded
-    (dict(sk=rb.Strides(HK * N * D + 4, N * D, D)), -7),    # 8-byte stride in bf16
-    (dict(sk=rb.Strides(1 << 40, N * D, D)), -1),
-    (dict(ws_bytes=0), -4), (dict(ws=None), -4), (dict(ws=FAKE + 8), -7),
+    (dict(scale=math.nan), -1), (dict(scale=math.inf), -1), (dict(dtype=7), -3),
+    (dict(q=rows(H, 0)), -1), (dict(v=rows(HK, FAKE + 8)), -7), (dict(g=0), -1),
+    (dict(S0=FAKE + 4), -7), (dict(last=FAKE + 8), -7),
+    (dict(q=(FAKE, H * N * D, N * D, D - 8)), -1),     # rows overlap
+    (dict(k=(FAKE, HK * N * D, 0, D)), -1),            # heads expanded
+    (dict(k=(FAKE, HK * N * D + 4, N * D, D)), -7),    # 8-byte stride in bf16
+    (dict(k=(FAKE, 1 << 40, N * D, D)), -1),
+    (dict(ws_bytes=0), -4), (dict(ws=0), -4), (dict(ws=FAKE + 8), -7),
 ])
 def test_decay_forward_refuses(lib, kw, status):
     assert decay(lib, **kw) == status
@@ -61,16 +57,16 @@ def test_decay_forward_refuses(lib, kw, status):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(Hk=3), -1), (dict(D=12), -2), (dict(dout=None), -1), (dict(dk=None), -1),
-    (dict(dv=FAKE + 2), -7), (dict(ws_bytes=64), -4),
+    (dict(Hk=3), -1), (dict(D=12), -2), (dict(dout=rows(H, 0)), -1),
+    (dict(dk=rows(HK, 0)), -1), (dict(dv=rows(HK, FAKE + 2)), -7), (dict(ws_bytes=64), -4),
 ])
 def test_decay_backward_refuses(lib, kw, status):
     assert decay(lib, "backward", **kw) == status
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(state=None), -1), (dict(g=None), -1), (dict(pool=0), -1), (dict(pool=1), -1),
-    (dict(state=FAKE + 8), -7), (dict(out=None), -1), (dict(D=4), -2), (dict(dt=2), -3),
+    (dict(state=0), -1), (dict(g=0), -1), (dict(pool=0), -1), (dict(pool=1), -1),
+    (dict(state=FAKE + 8), -7), (dict(out=rows(H, 0)), -1), (dict(D=4), -2), (dict(dtype=2), -3),
 ])
 def test_decay_step_refuses(lib, kw, status):
     assert decay(lib, "step", **kw) == status
@@ -79,27 +75,35 @@ def test_decay_step_refuses(lib, kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(B=0), -1), (dict(n=-1), -1), (dict(Hq=0), -1), (dict(Hk=-1), -1), (dict(R=0), -2),
     (dict(R=7), -2), (dict(R=66), -2), (dict(axes=0), -1), (dict(axes=5), -1),
-    (dict(scale=math.nan), -1), (dict(dt=3), -3), (dict(q=None), -1), (dict(freq=None), -1),
-    (dict(k=None), -1), (dict(q_out=FAKE, sqo=st(H, N + 1)), -1),
+    (dict(scale=math.nan), -1), (dict(dtype=3), -3), (dict(q=rows(H, 0)), -1),
+    (dict(freq=0), -1), (dict(k=rows(HK, 0)), -1), (dict(q_out=(FAKE, H * N * D, 8, D)), -1),
 ])
 def test_rotary_refuses(lib, kw, status):
-    names = [f[0] for f in rb.RotaryArgs._fields_]
-    a = dict(zip(names, (B, N, H, HK, D, D, 0, 0, 1, 0, 1, 0, 0, 0, 0, 1.0)))
-    a.update({n: kw[n] for n in kw if n in a})
-    g = lambda n, d: kw[n] if n in kw else d  # noqa: E731
-    assert lib.rehyat_rotary(rb.RotaryArgs(*a.values()), g("dt", rb.REHYAT_BF16), g("q", FAKE),
-                             st(H), g("k", FAKE), st(HK), g("freq", FAKE), None, None,
-                             g("q_out", FAKE + 1024), g("sqo", st(H)), FAKE, st(HK),
-                             None) == status
+    a = dict(B=B, n=N, Hq=H, Hk=HK, D=D, R=D, interleaved=0, inverse=0, axes=1, pos64=0,
+             add_index=1, dtype=rb.REHYAT_BF16, pos_axis=0, pos_batch=0, pos_token=0, start=0,
+             freq=FAKE, axis=0, pos=0, q=rows(H), k=rows(HK), q_out=rows(H, FAKE + 1024),
+             k_out=rows(HK), scale=1.0)
+    a.update(kw)
+    flat = [y for x in a.values() for y in (x if isinstance(x, tuple) else (x,))]
+    assert lib.rehyat_rotary(rb._ROTARY.pack(*flat), None) == status
     assert lib.rehyat_last_error().decode()
 
 
+def test_argument_blocks_match_the_header(lib):
+    """The sizes that the library asserts for its argument blocks; a null block is refused."""
+    assert [x.size for x in (rb._ROTARY, rb._DECAY_FORWARD, rb._DECAY_BACKWARD,
+                             rb._DECAY_STEP)] == [240, 208, 312, 184]
+    for name in ("rotary", "decay_forward", "decay_backward", "decay_step"):
+        assert getattr(lib, "rehyat_" + name)(None, None) == -1
+
+
 def test_workspace_grows_with_shared_heads_only_for_gradients(lib):
-    size = lambda Hk, bwd: rb.decay_workspace_size(  # noqa: E731
-        rb.DecayArgs(1, 4, Hk, 1000, 64, 1.0), rb.REHYAT_BF16, bwd)
+    size = lambda Hk, bwd: rb.decay_workspace_size(1, 4, Hk, 1000, 64, bwd)  # noqa: E731
     assert size(4, False) == size(2, False)
     assert size(2, True) - size(4, True) == 4 * 1000 * 64 * 4
-    assert rb.decay_workspace_size(rb.DecayArgs(1, 4, 4, 0, 64, 1.0), 0) > 0
+    assert rb.decay_workspace_size(1, 4, 4, 0, 64) > 0
+    with pytest.raises(rb.RehyatError):
+        rb.decay_workspace_size(1, 4, 3, 10, 64)
 
 
 def x(heads=H, n=N, d=D, dtype=torch.bfloat16):
