@@ -50,20 +50,26 @@ __device__ __forceinline__ uint32_t f2_bf16(uint64_t v) {
   f2_unpack(v, a, b);
   return pack_bf16x2(a, b);
 }
-// Eight bf16 values times w, rounded to bf16; with kTwo the rounding's remainder in a second part.
-template <bool kTwo>
+// Eight bf16 values times w in two bf16 parts: the rounded product and what the rounding left.
 __device__ __forceinline__ uint4 scale8(uint4 x, float w, uint4& lo) {
-  uint32_t in[4] = {x.x, x.y, x.z, x.w}, hi[4], rest[4];
+  const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+  uint32_t hi[4], rest[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     // a bf16 is the upper half of an fp32
     const uint64_t f = f2_mul(f2_bits(in[i] << 16, in[i] & 0xffff0000u), f2_pack(w, w));
     hi[i] = f2_bf16(f);
-    if (kTwo)
-      rest[i] = f2_bf16(f2_fma(f2_bits(hi[i] << 16, hi[i] & 0xffff0000u), f2_pack(-1.f, -1.f), f));
+    rest[i] = f2_bf16(f2_fma(f2_bits(hi[i] << 16, hi[i] & 0xffff0000u), f2_pack(-1.f, -1.f), f));
   }
-  if (kTwo) lo = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+  lo = make_uint4(rest[0], rest[1], rest[2], rest[3]);
   return make_uint4(hi[0], hi[1], hi[2], hi[3]);
+}
+// Eight bf16 values times a bf16 weight.
+__device__ __forceinline__ uint4 mul8(uint4 x, __nv_bfloat162 w) {
+  __nv_bfloat162* v = reinterpret_cast<__nv_bfloat162*>(&x);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __hmul2(v[i], w);
+  return x;
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -213,7 +219,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
         for (int j = 0; j < 4; ++j) {
           x[j] = *reinterpret_cast<uint4*>(hi + sw128_offset(r, c0 + j * 8, kRows));
           if (!valid) x[j] = make_uint4(0, 0, 0, 0);  // padding may hold anything
-          x[j] = scale8<true>(x[j], w, rest[j]);
+          x[j] = scale8(x[j], w, rest[j]);
         }
         if (i > 0) ok = wait(kLoFree + half, (i - 1) & 1);
         if (!ok) break;
@@ -268,7 +274,8 @@ constexpr uint32_t kColP = 0, kColIn = 128, kColSt = 256, kColAdd = 384;
 //   scores = a b^T -> P = sp L^|i-j| scores on the past, bf16, into TMEM     (warps 0-7)
 //   b weighted in place (after the scores have read it)                       (warps 8-15)
 //   add = b^T c;  in = P c;  st = a S                                         (warp 17)
-//   out = in + si L^(t+e) st -> over a's tile -> global                       (warps 0-7, 18)
+//   out = in + si L^(t+e) st -> over c's tile -> global                       (warps 0-7, 18)
+// (over c's, which the next product needs last: over a's, the next load of a came 1,100 clk late)
 //   S = L^rows S + add, in registers (half a row a thread), bf16 copy for a S (warps 8-15)
 // grid (nseg, B*H), block 608.
 template <bool kReverse, bool kOutF32>
@@ -279,7 +286,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                            const __grid_constant__ CUtensorMap tmOut, const Pass p) {
   enum {
     kAFull = 0, kBFull = 2, kCFull = 4, kAEmpty = 6, kBEmpty = 8, kCEmpty = 10, kScores = 12,
-    kPReady, kBReady, kOFull, kOFree, kAddFull, kSReady, kStaged, kDone, kNum
+    kPReady, kBReady, kOFull, kAddFull, kStaged, kDone, kNum
   };
   const int seg = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh - b * p.H;
   const int r_begin = seg * p.seg_rows, r_stop = min(r_begin + p.seg_rows, p.N);
@@ -315,7 +322,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
   }
   if (tid == 0) {
     for (int i = 0; i < kNum; ++i) {
-      const bool many = i == kPReady || i == kBReady || i == kOFree || i == kSReady || i == kStaged;
+      const bool many = i == kPReady || i == kBReady || i == kStaged;
       mbar_init(&bars[i], many ? 256 : 1);
     }
     abort_sh = 0;
@@ -354,7 +361,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       ++n;
     };
     for (int i = 0; i < nc && ok; ++i) {
-      load(i, kBFull, kBEmpty, 1, &tmB, hb, p.H / p.b.group, n_b);
+      load(i, kBFull, kBEmpty, 1, &tmB, hb, p.H / p.b.group, n_b);  // in the order they come free
       if (ok) load(i, kAFull, kAEmpty, 0, &tmA, ha, p.H / p.a.group, n_a);
       if (ok) load(i, kCFull, kCEmpty, 2, &tmC, hc, p.H / p.c.group, n_c);
     }
@@ -391,7 +398,8 @@ __global__ void __launch_bounds__(kRwThreads, 1)
     for (int i = 0; i < nc && ok; ++i) {
       const int s = i & 1;
       const bool last = i + 1 == nc, reads_state = i > 0 || carried;
-      // kBReady follows the arrival of chunk i - 1's sum in registers: its columns are free
+      // the threads that arrive on kBReady have read chunk i - 1's sum out of TMEM and published
+      // the state before; those of kPReady have read chunk i - 1's outputs
       ok = wait(kCFull + s, (i >> 1) & 1) && wait(kBReady, i & 1);
       if (!ok) break;
       tc_fence_after();
@@ -404,15 +412,13 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       }
       mma_commit_by(leader, &bars[kBEmpty + s]);
       __syncwarp();
-      ok = wait(kPReady, i & 1) && wait(kSReady, i & 1);
-      if (ok && i > 0) ok = wait(kOFree, (i - 1) & 1);
+      ok = wait(kPReady, i & 1);
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
       for (int kk = 0; kk < kRows / 16; ++kk)
         mma_ts_by(leader, tmem + kColIn, tmem + kColP + (kk >> 2) * 64 + (kk & 3) * 8,
                   mnmajor_desc(tile(i, 2), kk), id_o, kk > 0 ? 1u : 0u);
-      mma_commit_by(leader, &bars[kCEmpty + s]);
       if (reads_state) {
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
@@ -421,6 +427,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                       kk > 0 ? 1u : 0u);
       }
       mma_commit_by(leader, &bars[kOFull]);
+      mma_commit_by(leader, &bars[kAEmpty + s]);
       __syncwarp();
       if (!last) ok = scores(i + 1);
     }
@@ -428,21 +435,21 @@ __global__ void __launch_bounds__(kRwThreads, 1)
     __syncwarp();
     mbar_wait_drain(&bars[kDone], 0);
     __syncwarp();
-  } else if (warp == kRwOut) {  // ---- copies out; a's tile is free once its output has left ----
+  } else if (warp == kRwOut) {  // ---- copies out; c's tile is free once the output has left it ----
     bool ok = true;
     for (int i = 0; i < nc && ok; ++i) {
       ok = wait(kStaged, i & 1);
       if (!ok) break;
       if (lane == 0) {
         if (!kOutF32) {
-          const uint8_t* src = sm + (i & 1) * kRwStage;
+          const uint8_t* src = sm + (i & 1) * kRwStage + 2 * kTile;
           tma_store_4d_chk(56, &tmOut, src, 0, chunk_row(i), h, b, p.N, p.H, p.B);
           if (p.D > 64)
             tma_store_4d_chk(56, &tmOut, src + kRows * 128, 64, chunk_row(i), h, b, p.N, p.H, p.B);
           bulk_commit_group();
           bulk_wait_read_all();
         }
-        mbar_arrive(&bars[kAEmpty + (i & 1)]);
+        mbar_arrive(&bars[kCEmpty + (i & 1)]);
       }
       __syncwarp();
     }
@@ -465,23 +472,23 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       ok = wait(kScores, i & 1);
       if (!ok) break;
       tc_fence_after();
-      // 16 columns a turn; a warp's P (64 columns' bf16 pairs: 32 TMEM columns) lies over its own
+      // 32 columns a turn; a warp's P (64 columns' bf16 pairs: 32 TMEM columns) lies over its own
       // half of the scores, behind the columns already read
 #pragma unroll 1
-      for (int e = 0; e < 4; ++e) {
-        const int c0 = half * 64 + e * 16, jb = c0 >> 5;
-        uint32_t pk[8];
+      for (int q = 0; q < 2; ++q) {
+        const int jb = half * 2 + q;
+        uint32_t pk[16];
         if (kReverse ? jb < rw : jb > rw) {  // no past here
 #pragma unroll
-          for (int j = 0; j < 8; ++j) pk[j] = 0u;
+          for (int j = 0; j < 16; ++j) pk[j] = 0u;
         } else {
-          uint32_t v[16];
-          tmem_ld16(tmem + lanes + kColP + c0, v);
+          uint32_t v[32];
+          tmem_ld32(tmem + lanes + kColP + jb * 32, v);
           if (jb == rw || (kReverse && rows < kRows)) {
-            const int d0 = kReverse ? c0 - r : r - c0;
-            const int stop = rows - c0;
+            const int d0 = kReverse ? jb * 32 - r : r - jb * 32;
+            const int stop = rows - jb * 32;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 16; ++j) {
               float f[2];
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
@@ -492,14 +499,19 @@ __global__ void __launch_bounds__(kRwThreads, 1)
               pk[j] = pack_bf16x2(f[0], f[1]);
             }
           } else {
-            const float edge = p.sp * ex2(g2 * (float)(kReverse ? c0 - r : r - c0 - 15));
-            const uint64_t edge2 = f2_pack(edge, edge);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              pk[j] = f2_bf16(f2_mul(f2_mul(edge2, within[j]), f2_bits(v[2 * j], v[2 * j + 1])));
+            for (int e = 0; e < 2; ++e) {
+              const int c0 = jb * 32 + e * 16;
+              const float edge = p.sp * ex2(g2 * (float)(kReverse ? c0 - r : r - c0 - 15));
+              const uint64_t edge2 = f2_pack(edge, edge);
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                pk[e * 8 + j] = f2_bf16(f2_mul(f2_mul(edge2, within[j]),
+                                               f2_bits(v[e * 16 + 2 * j], v[e * 16 + 2 * j + 1])));
+            }
           }
         }
-        tmem_st8(tmem + lanes + kColP + half * 64 + e * 8, pk);
+        tmem_st16(tmem + lanes + kColP + half * 64 + q * 16, pk);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -513,32 +525,32 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       ok = wait(kOFull, i & 1);
       if (!ok) break;
       tc_fence_after();
-      uint8_t* stage = sm + (i & 1) * kRwStage;
+      uint8_t* stage = sm + (i & 1) * kRwStage + 2 * kTile;
       float* of = kOutF32 ? static_cast<float*>(p.out) + b * p.ob + h * p.oh + (row0 + r) * p.on
                           : nullptr;
       const int c_end = min(half * 64 + 64, p.D);
 #pragma unroll 1
-      for (int c0 = half * 64; c0 < c_end; c0 += 16) {
-        uint64_t o[8];
+      for (int c0 = half * 64; c0 < c_end; c0 += 32) {
+        uint64_t o[16];
         if (reads_state) {
-          uint32_t v[32];
-          tmem_ld16_pair(tmem + lanes + kColIn + c0, tmem + lanes + kColSt + c0, v);
+          uint32_t v[32], w[32];
+          tmem_ld32_pair(tmem + lanes + kColIn + c0, tmem + lanes + kColSt + c0, v, w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            o[j] = f2_fma(f2, f2_bits(v[16 + 2 * j], v[17 + 2 * j]), f2_bits(v[2 * j], v[2 * j + 1]));
+          for (int j = 0; j < 16; ++j)
+            o[j] = f2_fma(f2, f2_bits(w[2 * j], w[2 * j + 1]), f2_bits(v[2 * j], v[2 * j + 1]));
         } else {
-          uint32_t v[16];
-          tmem_ld16(tmem + lanes + kColIn + c0, v);
+          uint32_t v[32];
+          tmem_ld32(tmem + lanes + kColIn + c0, v);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = f2_bits(v[2 * j], v[2 * j + 1]);
+          for (int j = 0; j < 16; ++j) o[j] = f2_bits(v[2 * j], v[2 * j + 1]);
         }
         if (!valid)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = 0ull;
+          for (int j = 0; j < 16; ++j) o[j] = 0ull;
         if (kOutF32) {
           if (row0 + r < r_stop)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 8; ++j)
               if (c0 + j * 4 < p.D) {
                 float4 x;
                 f2_unpack(o[2 * j], x.x, x.y);
@@ -547,14 +559,13 @@ __global__ void __launch_bounds__(kRwThreads, 1)
               }
         } else {
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < 4; ++j)
             *reinterpret_cast<uint4*>(stage + sw128_offset(r, c0 + j * 8, kRows)) =
                 make_uint4(f2_bf16(o[4 * j]), f2_bf16(o[4 * j + 1]), f2_bf16(o[4 * j + 2]),
                            f2_bf16(o[4 * j + 3]));
         }
       }
       tc_fence_before();
-      mbar_arrive(&bars[kOFree]);
       fence_async_smem();
       mbar_arrive(&bars[kStaged]);
     }
@@ -571,8 +582,6 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       for (int j = 0; j < 8; ++j)
         *reinterpret_cast<uint4*>(sS + sw128_offset(r, c0 + j * 8, kRows)) = make_uint4(
             f2_bf16(S[j * 4]), f2_bf16(S[j * 4 + 1]), f2_bf16(S[j * 4 + 2]), f2_bf16(S[j * 4 + 3]));
-      fence_async_smem();
-      mbar_arrive(&bars[kSReady]);
     };
     grid_dep_wait();  // the prefix comes from the launch before
     if (carried && r < p.D) {
@@ -600,7 +609,11 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       const int rows = min(kRows, r_end - chunk_row(i));
       const int t = kReverse ? rows - 1 - r : r;
       const bool valid = r < rows;
-      const float w = valid ? p.sd * ex2(g2 * (float)(rows - t - p.e)) : 0.f;
+      // The weight is rounded to bf16 before the product is: one rounding more on the way through the
+      // carried state (two of b, the state's copy, the output: 2^-8 / sqrt(3) * sqrt(4) = 4.5e-3 at
+      // most in the mean square), for a quarter of the instructions.
+      const __nv_bfloat162 w2 = __float2bfloat162_rn(valid ? p.sd * ex2(g2 * (float)(rows - t - p.e))
+                                                           : 0.f);
       uint8_t* tb = sm + s * kRwStage + kTile;
       ok = wait(kScores, i & 1) && wait(kCFull + s, (i >> 1) & 1);
       if (!ok) break;
@@ -609,10 +622,10 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         for (int c = c0; c < c0 + 64; c += 16) {
           uint4* q0 = reinterpret_cast<uint4*>(tb + sw128_offset(r, c, kRows));
           uint4* q1 = reinterpret_cast<uint4*>(tb + sw128_offset(r, c + 8, kRows));
-          uint4 x = *q0, y = *q1, none;
+          uint4 x = *q0, y = *q1;
           if (!valid) x = y = make_uint4(0, 0, 0, 0);
-          *q0 = scale8<false>(x, w, none);
-          *q1 = scale8<false>(y, w, none);
+          *q0 = mul8(x, w2);
+          *q1 = mul8(y, w2);
         }
       }
       if (!valid)  // padding may hold anything, and P's zeros must not meet it

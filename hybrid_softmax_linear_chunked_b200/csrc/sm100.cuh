@@ -441,15 +441,18 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
       : "r"(taddr), "r"(taddr + 32)
       : "memory");
 }
-// Load 16 consecutive columns from each of two places (into r[0, 16) and r[16, 32)) with one wait.
-__device__ __forceinline__ void tmem_ld16_pair(uint32_t taddr0, uint32_t taddr1, uint32_t (&r)[32]) {
+// Load 32 consecutive columns from each of two places with one wait.
+__device__ __forceinline__ void tmem_ld32_pair(uint32_t taddr0, uint32_t taddr1,
+                                               uint32_t (&r0)[32], uint32_t (&r1)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15}, [%32];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, "
-      "%26, %27, %28, %29, %30, %31}, [%33];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, "
+      "%41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, "
+      "%58, %59, %60, %61, %62, %63}, [%65];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : REHYAT_R32(r, 0)
+      : REHYAT_R32(r0, 0), REHYAT_R32(r1, 0)
       : "r"(taddr0), "r"(taddr1)
       : "memory");
 }
