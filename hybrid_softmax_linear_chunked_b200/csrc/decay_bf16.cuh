@@ -50,16 +50,18 @@ __device__ __forceinline__ uint32_t f2_bf16(uint64_t v) {
   f2_unpack(v, a, b);
   return pack_bf16x2(a, b);
 }
-// Eight bf16 values times w in two bf16 parts: the rounded product and what the rounding left.
+// Eight bf16 values times w, rounded to bf16; with kTwo what the rounding left in a second part.
+template <bool kTwo>
 __device__ __forceinline__ uint4 scale8(uint4 x, float w, uint4& lo) {
   const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-  uint32_t hi[4], rest[4];
+  uint32_t hi[4], rest[4] = {};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     // a bf16 is the upper half of an fp32
     const uint64_t f = f2_mul(f2_bits(in[i] << 16, in[i] & 0xffff0000u), f2_pack(w, w));
     hi[i] = f2_bf16(f);
-    rest[i] = f2_bf16(f2_fma(f2_bits(hi[i] << 16, hi[i] & 0xffff0000u), f2_pack(-1.f, -1.f), f));
+    if (kTwo)
+      rest[i] = f2_bf16(f2_fma(f2_bits(hi[i] << 16, hi[i] & 0xffff0000u), f2_pack(-1.f, -1.f), f));
   }
   lo = make_uint4(rest[0], rest[1], rest[2], rest[3]);
   return make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -76,26 +78,30 @@ __device__ __forceinline__ uint4 mul8(uint4 x, __nv_bfloat162 w) {
 // States: delta = sd * sum_j L^(n - t_j - e) b_j c_j^T over a segment.
 // ---------------------------------------------------------------------------------------------
 constexpr int kStStages = 3;
-constexpr int kStMath = 256;                 // warps 0-7: weigh b, split it in two parts
-constexpr int kStThreads = kStMath + 64;     // warp 8: copies, warp 9: products
+constexpr int kStHalf = 256;                   // warps 0-7 weigh rows 0-63 of a chunk, 8-15 the rest
+constexpr int kStIn = 16, kStMma = 17;         // copies, products
+constexpr int kStThreads = 2 * kStHalf + 64;
 constexpr uint32_t kStOffLo = kStStages * 2 * kTile;
 constexpr uint32_t kStSmem = kStOffLo + kTile + 1024;
 static_assert(kStSmem + 256 <= 232448, "shared memory over the limit");
 
 // Every weight is taken to the segment's end, so chunks add up without rescaling, in any order.
 // They run in the order opposite to the row pass that follows: what was read last (and may still be
-// in L2) is read first there.  A chunk is weighed and multiplied in two halves of 64 rows, so that
-// the products of one run while the other is weighed (one half's remainders fit beside three
-// stages).  The tensor core's own accumulation truncates, which shows in fp32 sums over thousands
-// of rows (8.6e-6 of the state after 12,600 rows); every kFlush chunks the sum moves to registers.
-// grid (nseg, B*H), block 320.
+// in L2) is read first there.  The two halves of a chunk have their own warps and barriers, so one
+// is weighed while the other is multiplied.
+// kTwo: weighted rows in two bf16 parts, for a last state good to fp32; without, in one, for sums
+// that only the row pass reads (it rounds the state to bf16 anyway).
+// The tensor core's own accumulation truncates, which shows in fp32 sums over thousands of rows
+// (8.6e-6 of the state after 12,600 rows); every kFlush chunks the sum moves to registers.
+// grid (nseg, B*H), block 576.
 constexpr int kFlush = 8;
+template <bool kTwo>
 __global__ void __launch_bounds__(kStThreads, 1)
     decay_states_bf16_kernel(const __grid_constant__ CUtensorMap tmB,
                              const __grid_constant__ CUtensorMap tmC, const Pass p) {
   enum {
-    kFull = 0, kEmpty = kFull + kStStages, kReady = kEmpty + kStStages, kLoFree = kReady + 2,
-    kDone = kLoFree + 2, kNum
+    kFull = 0, kEmpty = kFull + kStStages, kReady = kEmpty + kStStages,  // kReady: [half][stage]
+    kLoFree = kReady + 2 * kStStages, kSummed = kLoFree + 2, kDone, kNum
   };
   grid_dep_signal();
   const int seg = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh - b * p.H;
@@ -111,12 +117,13 @@ __global__ void __launch_bounds__(kStThreads, 1)
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
   volatile int* abort_flag = &abort_sh;
-  if (warp == 8) {
+  if (warp == kStIn) {
     tmem_alloc(&tmem_sh, 128);
     tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < kNum; ++i) mbar_init(&bars[i], i == kReady || i == kReady + 1 ? kStMath : 1);
+    for (int i = 0; i < kNum; ++i)
+      mbar_init(&bars[i], i >= kReady && i < kLoFree ? kStHalf : 1);
     abort_sh = 0;
     fence_mbar_init();
   }
@@ -129,7 +136,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
   };
   auto chunk_row = [&](int i) { return r_begin + (p.reverse ? i : nc - 1 - i) * kRows; };
 
-  if (warp == 8) {  // ---- copies ----
+  if (warp == kStIn) {  // ---- copies ----
     const int hb = h / p.b.group, hc = h / p.c.group;
     bool ok = true;
     int issued = 0;
@@ -150,15 +157,17 @@ __global__ void __launch_bounds__(kStThreads, 1)
       for (int i = max(0, issued - kStStages); i < issued; ++i)
         mbar_wait_drain(&bars[kFull + i % kStStages], (i / kStStages) & 1);
     __syncwarp();
-  } else if (warp == 9) {  // ---- products: b^T c, high and low part of b ----
+  } else if (warp == kStMma) {  // ---- products: b^T c, both parts of b ----
     const int w = (p.D + 15) / 16 * 16;
     const uint32_t id = idesc_bf16(128, w, true, true);
     const uint32_t sm0 = smem_u32(sm), lo = sm0 + kStOffLo, leader = elect_lane();
     bool ok = true;
     for (int i = 0; i < nc && ok; ++i) {
       const int s = i % kStStages;
+      // a new sum begins once every thread has read the one before out of TMEM, either half's
+      if (i > 0 && i % kFlush == 0) ok = wait(kReady + kStStages + s, (i / kStStages) & 1);
       for (int half = 0; half < 2 && ok; ++half) {
-        ok = wait(kReady + half, i & 1);
+        ok = wait(kReady + half * kStStages + s, (i / kStStages) & 1);
         if (!ok) break;
         tc_fence_after();
         const uint32_t hi = sm0 + s * 2 * kTile, c = hi + kTile;
@@ -167,10 +176,12 @@ __global__ void __launch_bounds__(kStThreads, 1)
           const int kk = half * 4 + k4;
           mma_ss_by(leader, tmem, mnmajor_desc(hi, kk), mnmajor_desc(c, kk), id,
                     (i % kFlush > 0 || kk > 0) ? 1u : 0u);
-          mma_ss_by(leader, tmem, mnmajor_desc(lo, kk), mnmajor_desc(c, kk), id, 1u);
+          if (kTwo)
+            mma_ss_by(leader, tmem, mnmajor_desc(lo, kk), mnmajor_desc(c, kk), id, 1u);
         }
-        mma_commit_by(leader, &bars[kLoFree + half]);
+        if (kTwo) mma_commit_by(leader, &bars[kLoFree + half]);
         if (half) mma_commit_by(leader, &bars[kEmpty + s]);
+        if (half && (i + 1) % kFlush == 0) mma_commit_by(leader, &bars[kSummed]);
         __syncwarp();
       }
     }
@@ -179,60 +190,55 @@ __global__ void __launch_bounds__(kStThreads, 1)
     mbar_wait_drain(&bars[kDone], 0);
     __syncwarp();
   } else {  // ---- weights: a row of a half chunk, 32 columns a thread ----
-    const int r64 = tid & 63, c0 = (tid >> 6) * 32;
+    const int half = warp >> 3, r = half * 64 + (tid & 63), c0 = ((tid >> 6) & 3) * 32;
     const float g2 = log2_decay(p.log_decay, h);
-    // the sum: row (TMEM lane) rs, columns cs .. cs + 63
-    const int rs = tid & 127, cs = (tid >> 7) * 64;
+    // the sum: row (TMEM lane) rs, columns cs .. cs + 31
+    const int rs = tid & 127, cs = (tid >> 7) * 32;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    float sum[64];
+    float sum[32];
 #pragma unroll
-    for (int j = 0; j < 64; ++j) sum[j] = 0.f;
+    for (int j = 0; j < 32; ++j) sum[j] = 0.f;
     auto flush = [&]() {
       tc_fence_after();
+      uint32_t v[32];
+      tmem_ld32(tmem + lanes + cs, v);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t v[32];
-        tmem_ld32(tmem + lanes + cs + q * 32, v);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) sum[q * 32 + j] += __uint_as_float(v[j]);
-      }
+      for (int j = 0; j < 32; ++j) sum[j] += __uint_as_float(v[j]);
       tc_fence_before();
     };
     bool ok = true;
-    for (int i = 0; i < nc && ok; ++i) {
+    for (int i = 0; i < nc; ++i) {
       const int s = i % kStStages;
+      const int row = chunk_row(i) + r;
+      const bool valid = row < r_end;
+      const int m = p.reverse ? row - r_begin + 1 - p.e : r_end - p.e - row;
+      const float w = valid ? p.sd * exp2f(g2 * (float)m) : 0.f;
       ok = wait(kFull + s, (i / kStStages) & 1);
-      if (ok && i > 0 && i % kFlush == 0) {
-        ok = wait(kLoFree + 1, (i - 1) & 1);  // the products of every chunk before are complete
-        if (ok) flush();
-      }
+      if (!ok) break;
       uint8_t* hi = sm + s * 2 * kTile;
       uint8_t* lo = sm + kStOffLo;
-#pragma unroll 1
-      for (int half = 0; half < 2 && ok; ++half) {
-        const int r = half * 64 + r64, row = chunk_row(i) + r;
-        const bool valid = row < r_end;
-        const int m = p.reverse ? row - r_begin + 1 - p.e : r_end - p.e - row;
-        const float w = valid ? p.sd * exp2f(g2 * (float)m) : 0.f;
-        uint4 x[4], rest[4];
+      uint4 x[4], rest[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[j] = *reinterpret_cast<uint4*>(hi + sw128_offset(r, c0 + j * 8, kRows));
-          if (!valid) x[j] = make_uint4(0, 0, 0, 0);  // padding may hold anything
-          x[j] = scale8(x[j], w, rest[j]);
-        }
-        if (i > 0) ok = wait(kLoFree + half, (i - 1) & 1);
-        if (!ok) break;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t off = sw128_offset(r, c0 + j * 8, kRows);
-          *reinterpret_cast<uint4*>(hi + off) = x[j];
-          *reinterpret_cast<uint4*>(lo + off) = rest[j];
-          if (!valid) *reinterpret_cast<uint4*>(hi + kTile + off) = make_uint4(0, 0, 0, 0);
-        }
-        fence_async_smem();
-        mbar_arrive(&bars[kReady + half]);
+      for (int j = 0; j < 4; ++j) {
+        x[j] = *reinterpret_cast<uint4*>(hi + sw128_offset(r, c0 + j * 8, kRows));
+        if (!valid) x[j] = make_uint4(0, 0, 0, 0);  // padding may hold anything
+        x[j] = scale8<kTwo>(x[j], w, rest[j]);
       }
+      if (kTwo && i > 0) ok = wait(kLoFree + half, (i - 1) & 1);
+      if (ok && i > 0 && i % kFlush == 0) {
+        ok = wait(kSummed, (i / kFlush - 1) & 1);
+        if (ok) flush();
+      }
+      if (!ok) break;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t off = sw128_offset(r, c0 + j * 8, kRows);
+        *reinterpret_cast<uint4*>(hi + off) = x[j];
+        if (kTwo) *reinterpret_cast<uint4*>(lo + off) = rest[j];
+        if (!valid) *reinterpret_cast<uint4*>(hi + kTile + off) = make_uint4(0, 0, 0, 0);
+      }
+      fence_async_smem();
+      mbar_arrive(&bars[kReady + half * kStStages + s]);
     }
     if (ok) ok = wait(kDone, 0);
     if (ok) {
@@ -240,7 +246,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
       float* dst = p.delta + (((size_t)bh * p.nseg + seg) * p.D + rs) * p.D;
       if (rs < p.D) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
+        for (int j = 0; j < 8; ++j)
           if (cs + j * 4 < p.D)
             *reinterpret_cast<float4*>(dst + cs + j * 4) =
                 make_float4(sum[j * 4], sum[j * 4 + 1], sum[j * 4 + 2], sum[j * 4 + 3]);
@@ -249,7 +255,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kStIn) {
     tc_fence_after();
     tmem_dealloc(tmem, 128);
   }

@@ -143,17 +143,18 @@ struct Behind {
   }
 };
 
-int launch_decay_states(const Pass& p, rehyat_dtype dt, cudaStream_t st) {
+// exact: the last state will be given out, so bf16 sums are formed from two-part products.
+int launch_decay_states(const Pass& p, rehyat_dtype dt, bool exact, cudaStream_t st) {
   const dim3 grid(p.nseg, p.B * p.H);
   if (dt == REHYAT_BF16) {
     using namespace rehyat::decay::tc;
     CUtensorMap mb, mc;
     RH_TRY(map_of(&mb, p.b, p));
     RH_TRY(map_of(&mc, p.c, p));
-    RH_TRY(cuda_check(cudaFuncSetAttribute(decay_states_bf16_kernel,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+    auto k = exact ? decay_states_bf16_kernel<true> : decay_states_bf16_kernel<false>;
+    RH_TRY(cuda_check(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            (int)kStSmem), "decay states attr"));
-    decay_states_bf16_kernel<<<grid, kStThreads, kStSmem, st>>>(mb, mc, p);
+    k<<<grid, kStThreads, kStSmem, st>>>(mb, mc, p);
   } else {
     using namespace rehyat::decay;
     const int smem = states_smem_floats(padded(p.D)) * 4;
@@ -217,7 +218,7 @@ int decay_prefix(Pass p, rehyat_dtype dt, const float* S0, float* last, const fl
   }
   if (p.N > 0) {
     p.seg_skip = last ? -1 : (p.reverse ? 0 : p.nseg - 1);
-    RH_TRY(launch_decay_states(p, dt, st));
+    RH_TRY(launch_decay_states(p, dt, last != nullptr, st));
   }
   // the row pass reads the workspace's copy of S0, since `last` may be S0
   RH_TRY(launch_decay_scan(p, S0, last, many || S0, bf16 && p.N > 0, st));

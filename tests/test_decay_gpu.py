@@ -160,6 +160,25 @@ def test_prompt_and_gradients(dev, shape):
     check_backward(p, grads, scale)
 
 
+@pytest.mark.parametrize("dtype,H,N", [(torch.bfloat16, 150, 3100), (torch.bfloat16, 74, 4700),
+                                       (torch.float32, 150, 1000)], ids=str)
+def test_long_segments(dev, dtype, H, N):
+    """So many heads that a segment is 18 to 25 chunks long; three heads checked."""
+    heads = [0, H // 2, H - 1]
+    decays = [0.0 if h == H // 2 else -2.0 ** (-1 - h * 10 / H) for h in range(H)]
+    p = problem(dev, dtype, 1, H, H, N, 32, True, decays=decays, seed=19)
+    kw = dict(scale=0.125, state=p["S0"])
+    out, last = rb.decay_forward(p["q"], p["k"], p["v"], p["g"], final_state=True, **kw)
+    g = rb.decay_backward(p["q"], p["k"], p["v"], p["g"], p["dout"], dfinal=p["dS"], **kw)
+    no_state = rb.decay_backward(p["q"], p["k"], p["v"], p["g"], p["dout"], scale=0.125)
+    rb.sync_status(dev)
+    cut = {n: (x[heads] if n == "g" else x[:, heads]) for n, x in p.items()}
+    check_forward(cut, out[:, heads], last[:, heads], 0.125)
+    check_backward(cut, {n: x[:, heads] for n, x in g.items()}, 0.125)
+    cut["S0"] = cut["dS"] = None
+    check_backward(cut, {n: x[:, heads] for n, x in no_state.items()}, 0.125)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
 @pytest.mark.parametrize("N", [130, 700])
 def test_padded_batch(dev, dtype, N):
