@@ -68,6 +68,7 @@ def use_library(path: str) -> ctypes.CDLL:
     build, build.build(debug_bounds=True)); returns it loaded."""
     global _lib, _LIB_PATH
     _lib, _LIB_PATH = None, path
+    decay_workspace_size.cache_clear()
     return load()
 
 

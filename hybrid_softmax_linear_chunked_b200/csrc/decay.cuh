@@ -14,6 +14,10 @@
 // e says on which side of a range's border the state stands: S_0 has decayed once when row 0 reads
 // it, the gradient of the last state reaches the last row undecayed.
 //
+// States in the workspace are stored by column quads: elements (r, 4c .. 4c+3) at float4 c * D + r,
+// so that the kernels' threads, one row each, read and write neighbouring float4s (by rows, a state
+// took a row-pass CTA 3.8 us to read and a states CTA 2.9 us to write).
+//
 // A sequence is cut into segments of whole 128-row blocks.  Three launches: the sum of every
 // segment's own rows (decay_states), its exclusive prefix in time order (decay_scan), and the rows
 // of every segment, chunk after chunk with the state carried along (decay_rows).  Every exponent
@@ -50,14 +54,19 @@ struct Pass {
   long long ob, oh, on;      // its strides
   const float* log_decay;    // [H]
   const int* lengths;        // [B] or null: rows at and past a sequence's length are padding
-  const float* prefix;       // [B*H][nseg][D][D] state before each segment in time, or null (zero)
-  float* delta;              // [B*H][nseg][D][D] each segment's own sum (written by the states)
+  const float* prefix;       // [B*H][nseg] states before each segment in time, or null (zero)
+  float* delta;              // [B*H][nseg] states: each segment's own sum
   int B, H, N, D;
   int nseg, seg_rows;
   int reverse, e;
   int transposed;            // the pass's state is the transpose of `prefix`
   int seg_skip;              // states: the segment whose sum nothing reads, or -1
+  int exact;                 // states: the last state is given out (bf16: two-part products)
+  int out_f32;               // rows: fp32 output for the group sum
   float sp, si, sd;
+};
+struct Passes {  // of one launch: blockIdx.z
+  Pass p[3];
 };
 
 // log2 of the decay, bounded below so that 0 * log2(0) stays 0 (2^-1000 is 0 in fp32); NaN stays.
@@ -159,9 +168,12 @@ __device__ __forceinline__ int outer_row(const Outer& o, int i) {
 }
 
 // Each segment's own sum: delta = sd * sum_j L^(n - t_j - e) b_j c_j^T over its n valid rows.
-// grid (nseg, B*H), block 256.
-__global__ void __launch_bounds__(kThreads, 1) decay_states_kernel(const Pass p) {
+// grid (nseg, B*H, n), block 256.
+__global__ void __launch_bounds__(kThreads, 1)
+    decay_states_kernel(const __grid_constant__ Passes all) {
   extern __shared__ __align__(16) float smf[];
+  sm100::grid_dep_signal();
+  const Pass& p = all.p[blockIdx.z];
   const int seg = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh - b * p.H;
   if (seg == p.seg_skip) return;
   const int Dp = padded(p.D), ld = Dp + 4;
@@ -194,20 +206,36 @@ __global__ void __launch_bounds__(kThreads, 1) decay_states_kernel(const Pass p)
   for (int i = 0; i < 8; ++i) {
     const int r = outer_row(o, i);
     if (r >= p.D) continue;
-    if (o.j0 < p.D) store4(dst + (size_t)r * p.D + o.j0, acc[i][0]);
-    if (o.j0 + o.half < p.D) store4(dst + (size_t)r * p.D + o.j0 + o.half, acc[i][1]);
+    if (o.j0 < p.D) store4(dst + o.j0 * p.D + r * 4, acc[i][0]);
+    if (o.j0 + o.half < p.D) store4(dst + (o.j0 + o.half) * p.D + r * 4, acc[i][1]);
   }
 }
 
 // The state before each segment in time order, written over the segment's own sum, and the state
-// after the last: state_{s+1} = L^(rows of s) state_s + delta_s.  S0 and last may be the same
-// buffer (each element is read before it is written, by one thread).
-// grid (ceil(D*D/4 / 256), B*H), block 256.
-__global__ void __launch_bounds__(256)
-    decay_scan_kernel(float* delta, const float* S0, float* last, const float* log_decay,
-                      const int* lengths, int H, int N, int D, int nseg, int seg_rows, int reverse,
-                      int need_prefix) {
+// after the last: state_{s+1} = L^(rows of s) state_s + delta_s.  S0 and last are stored by rows and
+// may be the same buffer (each element is read before it is written, by one thread).
+struct Scan {
+  float* delta;
+  const float* S0;
+  float* last;
+  int reverse, need_prefix;
+};
+struct Scans {
+  Scan s[2];
+  const float* log_decay;
+  const int* lengths;
+  int H, N, D, nseg, seg_rows;
+};
+// grid (ceil(D*D/4 / 256), B*H, scans), block 256.
+__global__ void __launch_bounds__(256) decay_scan_kernel(const __grid_constant__ Scans a) {
   sm100::grid_dep_signal();
+  float* delta = a.s[blockIdx.z].delta;
+  const float* S0 = a.s[blockIdx.z].S0;
+  float* last = a.s[blockIdx.z].last;
+  const int reverse = a.s[blockIdx.z].reverse, need_prefix = a.s[blockIdx.z].need_prefix;
+  const int H = a.H, N = a.N, D = a.D, nseg = a.nseg, seg_rows = a.seg_rows;
+  const float* log_decay = a.log_decay;
+  const int* lengths = a.lengths;
   const int bh = blockIdx.y, b = bh / H, h = bh - b * H;
   const int i = blockIdx.x * 256 + threadIdx.x;
   const int n4 = D * D / 4;
@@ -216,7 +244,8 @@ __global__ void __launch_bounds__(256)
   const float g2 = log2_decay(log_decay, h);
   const int n = length_of(lengths, b, N);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (S0) acc = reinterpret_cast<const float4*>(S0)[(size_t)bh * n4 + i];
+  const int at = (i % D) * (D / 4) + i / D;  // of a state stored by rows
+  if (S0) acc = reinterpret_cast<const float4*>(S0)[(size_t)bh * n4 + at];
   float4* d = reinterpret_cast<float4*>(delta) + (size_t)bh * nseg * n4 + i;
   const int steps = last ? nseg : nseg - 1;  // the last segment's sum is only in the last state
   // eight segments' sums are loaded before any is written over, so their latencies overlap
@@ -237,14 +266,16 @@ __global__ void __launch_bounds__(256)
       if (t < steps && rows > 0) acc = fma4(exp2f(g2 * (float)rows), acc, add[u]);
     }
   }
-  if (last) reinterpret_cast<float4*>(last)[(size_t)bh * n4 + i] = acc;
+  if (last) reinterpret_cast<float4*>(last)[(size_t)bh * n4 + at] = acc;
 }
 
 // The rows of one segment: chunks of kC in time order, the state [D][D] carried in shared memory.
 // Bound by the fp32 pipes: 2 kC D (kC + 2 D) multiply-adds a chunk.
-// grid (nseg, B*H), block 256.
-__global__ void __launch_bounds__(kThreads, 1) decay_rows_kernel(const Pass p) {
+// grid (nseg, B*H, n), block 256.
+__global__ void __launch_bounds__(kThreads, 1)
+    decay_rows_kernel(const __grid_constant__ Passes all) {
   extern __shared__ __align__(16) float smf[];
+  const Pass& p = all.p[blockIdx.z];
   const int seg = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh - b * p.H;
   const int Dp = padded(p.D), ld = Dp + 4, ldp = kC + 4;
   float* sa = smf;
@@ -259,16 +290,18 @@ __global__ void __launch_bounds__(kThreads, 1) decay_rows_kernel(const Pass p) {
   const int r_end = min(r_stop, n);
   float* out = static_cast<float*>(p.out) + b * p.ob + h * p.oh;
 
+  sm100::grid_dep_wait();  // the prefix comes from the launch before
   for (int i = tid; i < Dp * (Dp / 4); i += kThreads) {
     const int r = i / (Dp / 4), c = (i - r * (Dp / 4)) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (p.prefix && r < p.D && c < p.D) {
       const float* src = p.prefix + ((size_t)bh * p.nseg + seg) * p.D * p.D;
-      if (p.transposed)
-        x = make_float4(src[(size_t)c * p.D + r], src[(size_t)(c + 1) * p.D + r],
-                        src[(size_t)(c + 2) * p.D + r], src[(size_t)(c + 3) * p.D + r]);
-      else
-        x = load4<float>(src + (size_t)r * p.D + c);
+      if (p.transposed) {
+        const float* col = src + (r >> 2) * 4 * p.D + c * 4 + (r & 3);
+        x = make_float4(col[0], col[4], col[8], col[12]);
+      } else {
+        x = load4<float>(src + c * p.D + r * 4);
+      }
     }
     *reinterpret_cast<float4*>(ss + r * ld + c) = x;
   }
@@ -401,21 +434,26 @@ __global__ void __launch_bounds__(kThreads, 1) decay_rows_kernel(const Pass p) {
 }
 
 // out[b, kv head, row] = sum over its `group` query heads of part [B][Hk * group][N][D] (fp32),
-// in head order.  grid (blocks over rows * D / 4, B*Hk), block 256.
+// in head order, for two tensors.  grid (blocks over rows * D / 4, B*Hk, 2), block 256.
+struct GroupSum {
+  const float* part[2];
+  void* out[2];
+  long long ob[2], oh[2], on[2];
+  int Hk, group, N, D;
+};
 template <typename T>
-__global__ void __launch_bounds__(256)
-    decay_group_sum_kernel(const float* part, T* out, long long ob, long long oh, long long on,
-                           int Hk, int group, int N, int D) {
-  const int bk = blockIdx.y, b = bk / Hk, hk = bk - b * Hk;
-  const int v4 = D / 4;
-  const long long total = (long long)N * v4;
-  const float4* src = reinterpret_cast<const float4*>(part) + (long long)bk * group * total;
+__global__ void __launch_bounds__(256) decay_group_sum_kernel(const __grid_constant__ GroupSum a) {
+  const int w = blockIdx.z, bk = blockIdx.y, b = bk / a.Hk, hk = bk - b * a.Hk;
+  const int v4 = a.D / 4;
+  const long long total = (long long)a.N * v4;
+  const float4* src = reinterpret_cast<const float4*>(a.part[w]) + (long long)bk * a.group * total;
+  T* out = static_cast<T*>(a.out[w]) + b * a.ob[w] + hk * a.oh[w];
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total;
        i += (long long)gridDim.x * 256) {
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int u = 0; u < group; ++u) acc = fma4(1.f, src[u * total + i], acc);
+    for (int u = 0; u < a.group; ++u) acc = fma4(1.f, src[u * total + i], acc);
     const long long r = i / v4;
-    store4(out + b * ob + hk * oh + r * on + (i - r * v4) * 4, acc);
+    store4(out + r * a.on[w] + (i - r * v4) * 4, acc);
   }
 }
 

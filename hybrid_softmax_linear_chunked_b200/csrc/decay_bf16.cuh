@@ -92,19 +92,18 @@ static_assert(kStSmem + 256 <= 232448, "shared memory over the limit");
 // kTwo: weighted rows in two bf16 parts, for a last state good to fp32; without, in one, for sums
 // that only the row pass reads (it rounds the state to bf16 anyway).
 // The tensor core's own accumulation truncates, which shows in fp32 sums over thousands of rows
-// (8.6e-6 of the state after 12,600 rows); every kFlush chunks the sum moves to registers.
-// grid (nseg, B*H), block 576.
-constexpr int kFlush = 8;
+// (8.6e-6 of the state after 12,600 rows).  So every kFlush chunks the sum goes on in the other of
+// two accumulators, and kLate chunks later, when its products are long complete, the first is added
+// to registers; it is written again only after both halves have weighed a later chunk.
+constexpr int kFlush = 8, kLate = 2;
 template <bool kTwo>
-__global__ void __launch_bounds__(kStThreads, 1)
-    decay_states_bf16_kernel(const __grid_constant__ CUtensorMap tmB,
-                             const __grid_constant__ CUtensorMap tmC, const Pass p) {
+__device__ __forceinline__ void states_of_segment(const CUtensorMap& tmB, const CUtensorMap& tmC,
+                                                  const Pass& p, int seg) {
   enum {
     kFull = 0, kEmpty = kFull + kStStages, kReady = kEmpty + kStStages,  // kReady: [half][stage]
     kLoFree = kReady + 2 * kStStages, kSummed = kLoFree + 2, kDone, kNum
   };
-  grid_dep_signal();
-  const int seg = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh - b * p.H;
+  const int bh = blockIdx.y, b = bh / p.H, h = bh - b * p.H;
   if (seg == p.seg_skip) return;
   const int r_begin = seg * p.seg_rows;
   const int r_end = min(r_begin + p.seg_rows, length_of(p.lengths, b, p.N));
@@ -118,7 +117,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
   __shared__ int abort_sh;
   volatile int* abort_flag = &abort_sh;
   if (warp == kStIn) {
-    tmem_alloc(&tmem_sh, 128);
+    tmem_alloc(&tmem_sh, 256);
     tmem_relinquish();
   }
   if (tid == 0) {
@@ -164,8 +163,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
     bool ok = true;
     for (int i = 0; i < nc && ok; ++i) {
       const int s = i % kStStages;
-      // a new sum begins once every thread has read the one before out of TMEM, either half's
-      if (i > 0 && i % kFlush == 0) ok = wait(kReady + kStStages + s, (i / kStStages) & 1);
+      const uint32_t sum = tmem + ((i / kFlush) & 1) * 128;
       for (int half = 0; half < 2 && ok; ++half) {
         ok = wait(kReady + half * kStStages + s, (i / kStStages) & 1);
         if (!ok) break;
@@ -174,10 +172,10 @@ __global__ void __launch_bounds__(kStThreads, 1)
 #pragma unroll
         for (int k4 = 0; k4 < 4; ++k4) {
           const int kk = half * 4 + k4;
-          mma_ss_by(leader, tmem, mnmajor_desc(hi, kk), mnmajor_desc(c, kk), id,
+          mma_ss_by(leader, sum, mnmajor_desc(hi, kk), mnmajor_desc(c, kk), id,
                     (i % kFlush > 0 || kk > 0) ? 1u : 0u);
           if (kTwo)
-            mma_ss_by(leader, tmem, mnmajor_desc(lo, kk), mnmajor_desc(c, kk), id, 1u);
+            mma_ss_by(leader, sum, mnmajor_desc(lo, kk), mnmajor_desc(c, kk), id, 1u);
         }
         if (kTwo) mma_commit_by(leader, &bars[kLoFree + half]);
         if (half) mma_commit_by(leader, &bars[kEmpty + s]);
@@ -198,10 +196,10 @@ __global__ void __launch_bounds__(kStThreads, 1)
     float sum[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) sum[j] = 0.f;
-    auto flush = [&]() {
+    auto flush = [&](int group) {
       tc_fence_after();
       uint32_t v[32];
-      tmem_ld32(tmem + lanes + cs, v);
+      tmem_ld32(tmem + lanes + (group & 1) * 128 + cs, v);
 #pragma unroll
       for (int j = 0; j < 32; ++j) sum[j] += __uint_as_float(v[j]);
       tc_fence_before();
@@ -225,9 +223,9 @@ __global__ void __launch_bounds__(kStThreads, 1)
         x[j] = scale8<kTwo>(x[j], w, rest[j]);
       }
       if (kTwo && i > 0) ok = wait(kLoFree + half, (i - 1) & 1);
-      if (ok && i > 0 && i % kFlush == 0) {
+      if (ok && i > kFlush && i % kFlush == kLate) {
         ok = wait(kSummed, (i / kFlush - 1) & 1);
-        if (ok) flush();
+        if (ok) flush(i / kFlush - 1);
       }
       if (!ok) break;
 #pragma unroll
@@ -242,13 +240,15 @@ __global__ void __launch_bounds__(kStThreads, 1)
     }
     if (ok) ok = wait(kDone, 0);
     if (ok) {
-      flush();
-      float* dst = p.delta + (((size_t)bh * p.nseg + seg) * p.D + rs) * p.D;
+      const int group = (nc - 1) / kFlush;
+      if (group > 0 && (nc - 1) % kFlush < kLate) flush(group - 1);
+      flush(group);
+      float* dst = p.delta + ((size_t)bh * p.nseg + seg) * p.D * p.D + rs * 4;
       if (rs < p.D) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           if (cs + j * 4 < p.D)
-            *reinterpret_cast<float4*>(dst + cs + j * 4) =
+            *reinterpret_cast<float4*>(dst + (cs + j * 4) * p.D) =
                 make_float4(sum[j * 4], sum[j * 4 + 1], sum[j * 4 + 2], sum[j * 4 + 3]);
       }
     }
@@ -257,8 +257,26 @@ __global__ void __launch_bounds__(kStThreads, 1)
   __syncthreads();
   if (warp == kStIn) {
     tc_fence_after();
-    tmem_dealloc(tmem, 128);
+    tmem_dealloc(tmem, 256);
   }
+}
+
+// The passes of one launch, one after the other (blockIdx.z): a pass fills the SMs that the one
+// before leaves idle at its end.  Interleaving them, so that passes over the same rows run side by
+// side, was slower (480x832 5 s gradients 385 us against 316).
+struct StatesArgs {
+  Pass p[2];
+  CUtensorMap b[2], c[2];
+};
+// grid (nseg, B*H, n), block 576.
+__global__ void __launch_bounds__(kStThreads, 1)
+    decay_states_bf16_kernel(const __grid_constant__ StatesArgs a) {
+  grid_dep_signal();
+  const int w = blockIdx.z, seg = blockIdx.x;
+  if (a.p[w].exact)
+    states_of_segment<true>(a.b[w], a.c[w], a.p[w], seg);
+  else
+    states_of_segment<false>(a.b[w], a.c[w], a.p[w], seg);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -283,18 +301,15 @@ constexpr uint32_t kColP = 0, kColIn = 128, kColSt = 256, kColAdd = 384;
 //   out = in + si L^(t+e) st -> over c's tile -> global                       (warps 0-7, 18)
 // (over c's, which the next product needs last: over a's, the next load of a came 1,100 clk late)
 //   S = L^rows S + add, in registers (half a row a thread), bf16 copy for a S (warps 8-15)
-// grid (nseg, B*H), block 608.
 template <bool kReverse, bool kOutF32>
-__global__ void __launch_bounds__(kRwThreads, 1)
-    decay_rows_bf16_kernel(const __grid_constant__ CUtensorMap tmA,
-                           const __grid_constant__ CUtensorMap tmB,
-                           const __grid_constant__ CUtensorMap tmC,
-                           const __grid_constant__ CUtensorMap tmOut, const Pass p) {
+__device__ __forceinline__ void rows_of_segment(const CUtensorMap& tmA, const CUtensorMap& tmB,
+                                                const CUtensorMap& tmC, const CUtensorMap& tmOut,
+                                                const Pass& p, int seg) {
   enum {
     kAFull = 0, kBFull = 2, kCFull = 4, kAEmpty = 6, kBEmpty = 8, kCEmpty = 10, kScores = 12,
     kPReady, kBReady, kOFull, kAddFull, kStaged, kDone, kNum
   };
-  const int seg = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh - b * p.H;
+  const int bh = blockIdx.y, b = bh / p.H, h = bh - b * p.H;
   const int r_begin = seg * p.seg_rows, r_stop = min(r_begin + p.seg_rows, p.N);
   const int r_end = min(r_stop, length_of(p.lengths, b, p.N));
   const int nc = max(0, (r_end - r_begin + kRows - 1) / kRows);  // chunks that hold valid rows
@@ -592,19 +607,34 @@ __global__ void __launch_bounds__(kRwThreads, 1)
     grid_dep_wait();  // the prefix comes from the launch before
     if (carried && r < p.D) {
       const float* src = p.prefix + ((size_t)bh * p.nseg + seg) * p.D * p.D;
+      // loads in batches, before any is used
       if (p.transposed) {
+        const float* col = src + (r >> 2) * 4 * p.D + c0 * 4 + (r & 3);
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (c0 + 2 * j < p.D)
-            S[j] = f2_pack(src[(size_t)(c0 + 2 * j) * p.D + r], src[(size_t)(c0 + 2 * j + 1) * p.D + r]);
+        for (int q = 0; q < 4; ++q) {
+          float x[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            x[j] = c0 + q * 16 + j < p.D ? col[(q * 16 + j) * 4] : 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) S[q * 8 + j] = f2_pack(x[2 * j], x[2 * j + 1]);
+        }
       } else {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (c0 + j * 4 < p.D) {
-            const float4 x = *reinterpret_cast<const float4*>(src + (size_t)r * p.D + c0 + j * 4);
-            S[j * 2] = f2_pack(x.x, x.y);
-            S[j * 2 + 1] = f2_pack(x.z, x.w);
+        for (int q = 0; q < 2; ++q) {
+          float4 x[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int c = c0 + q * 32 + j * 4;
+            x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c < p.D) x[j] = *reinterpret_cast<const float4*>(src + c * p.D + r * 4);
           }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            S[q * 16 + j * 2] = f2_pack(x[j].x, x[j].y);
+            S[q * 16 + j * 2 + 1] = f2_pack(x[j].z, x[j].w);
+          }
+        }
       }
     }
     publish();
@@ -665,6 +695,23 @@ __global__ void __launch_bounds__(kRwThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+struct RowsArgs {
+  Pass p[3];
+  CUtensorMap a[3], b[3], c[3], out[3];
+};
+// grid (nseg, B*H, n), block 608.
+__global__ void __launch_bounds__(kRwThreads, 1)
+    decay_rows_bf16_kernel(const __grid_constant__ RowsArgs a) {
+  const int w = blockIdx.z, seg = blockIdx.x;
+  const Pass& p = a.p[w];
+  if (!p.reverse)
+    rows_of_segment<false, false>(a.a[w], a.b[w], a.c[w], a.out[w], p, seg);
+  else if (!p.out_f32)
+    rows_of_segment<true, false>(a.a[w], a.b[w], a.c[w], a.out[w], p, seg);
+  else
+    rows_of_segment<true, true>(a.a[w], a.b[w], a.c[w], a.out[w], p, seg);
 }
 
 }  // namespace tc

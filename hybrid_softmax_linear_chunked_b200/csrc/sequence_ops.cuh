@@ -3,6 +3,8 @@
 // helpers (fail, RH_TRY, cuda_check, Carve).
 #pragma once
 
+#include <atomic>
+
 #include "decay.cuh"
 #include "decay_bf16.cuh"
 #include "rotary.cuh"
@@ -60,12 +62,13 @@ Rows rows_of(const rehyat_rows& s, int group) {
 }
 
 // Segments of a sequence: one CTA each, so their number trades whole waves of the 148 SMs against
-// the state pass that more than one segment needs (about half the work of the row pass).  `blocks`
-// 128-row blocks; +1 block a CTA for its start.
+// each CTA's start, which costs one to three chunks.  `blocks` of 128 rows.  A launch of three
+// passes takes the same cut: each pass fills the waves by itself (cut for all three at once, in one
+// wave of 64-chunk segments, the 480x832 5 s gradients took 380 us instead of 320).
 struct Segments {
   int n, rows;
 };
-Segments decay_segments(int BH, int N, bool states_anyway) {
+Segments decay_segments(int BH, int N) {
   const int blocks = (N + rehyat::decay::kBlockRows - 1) / rehyat::decay::kBlockRows;
   Segments best{1, blocks > 0 ? blocks * rehyat::decay::kBlockRows : rehyat::decay::kBlockRows};
   long long best_cost = -1;
@@ -74,7 +77,7 @@ Segments decay_segments(int BH, int N, bool states_anyway) {
     const int used = (blocks + per - 1) / per;  // segments that hold rows
     if (used != n) continue;
     const long long waves = ((long long)BH * n + 147) / 148;
-    const long long cost = waves * (per + 1) * (n > 1 || states_anyway ? 3 : 2);
+    const long long cost = waves * (per + 1);
     if (best_cost < 0 || cost < best_cost) {
       best_cost = cost;
       best = Segments{n, per * rehyat::decay::kBlockRows};
@@ -85,19 +88,19 @@ Segments decay_segments(int BH, int N, bool states_anyway) {
 
 struct DecayPlan {
   Segments seg;
-  size_t fwd, bwd, part, total;
+  size_t fwd, bwd, part[2], total;
 };
 DecayPlan plan_decay(const DecayDims& a, bool backward) {
   DecayPlan p{};
   const size_t BH = (size_t)a.B * a.H;
-  p.seg = decay_segments((int)BH, a.N, true);
+  p.seg = decay_segments((int)BH, a.N);
   Carve cv;
   const size_t states = BH * p.seg.n * a.D * a.D * 4;
   p.fwd = cv.take(states);
   if (backward) {
     p.bwd = cv.take(states);
     // per query head, where dk and dv are sums over the heads that share a key/value head
-    p.part = cv.take(a.H != a.Hk ? BH * (size_t)a.N * a.D * 4 : 0);
+    for (size_t& part : p.part) part = cv.take(a.H != a.Hk ? BH * (size_t)a.N * a.D * 4 : 0);
   }
   p.total = cv.off;
   return p;
@@ -143,88 +146,101 @@ struct Behind {
   }
 };
 
-// exact: the last state will be given out, so bf16 sums are formed from two-part products.
-int launch_decay_states(const Pass& p, rehyat_dtype dt, bool exact, cudaStream_t st) {
-  const dim3 grid(p.nseg, p.B * p.H);
+// Lets kernel kKernel use up to `most` bytes of dynamic shared memory, once on each device.
+template <auto kKernel>
+int allow_smem(int most) {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  RH_TRY(cuda_check(cudaGetDevice(&dev), "device"));
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return REHYAT_OK;
+  RH_TRY(cuda_check(cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most),
+                    "shared memory size"));
+  if (dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return REHYAT_OK;
+}
+
+// The passes of one launch: the states they need, and the rows.
+int launch_decay_states(const Pass* p, int n, rehyat_dtype dt, cudaStream_t st) {
+  const dim3 grid(p[0].nseg, p[0].B * p[0].H, n);
   if (dt == REHYAT_BF16) {
     using namespace rehyat::decay::tc;
-    CUtensorMap mb, mc;
-    RH_TRY(map_of(&mb, p.b, p));
-    RH_TRY(map_of(&mc, p.c, p));
-    auto k = exact ? decay_states_bf16_kernel<true> : decay_states_bf16_kernel<false>;
-    RH_TRY(cuda_check(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)kStSmem), "decay states attr"));
-    k<<<grid, kStThreads, kStSmem, st>>>(mb, mc, p);
+    StatesArgs a{};
+    for (int i = 0; i < n; ++i) {
+      a.p[i] = p[i];
+      RH_TRY(map_of(&a.b[i], p[i].b, p[i]));
+      RH_TRY(map_of(&a.c[i], p[i].c, p[i]));
+    }
+    RH_TRY(allow_smem<decay_states_bf16_kernel>(kStSmem));
+    decay_states_bf16_kernel<<<grid, kStThreads, kStSmem, st>>>(a);
   } else {
     using namespace rehyat::decay;
-    const int smem = states_smem_floats(padded(p.D)) * 4;
-    RH_TRY(cuda_check(cudaFuncSetAttribute(decay_states_kernel,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
-                      "decay states attr"));
-    decay_states_kernel<<<grid, kThreads, smem, st>>>(p);
+    Passes a{};
+    for (int i = 0; i < n; ++i) a.p[i] = p[i];
+    const int smem = states_smem_floats(padded(p[0].D)) * 4;
+    RH_TRY(allow_smem<decay_states_kernel>(states_smem_floats(kMaxD) * 4));
+    decay_states_kernel<<<grid, kThreads, smem, st>>>(a);
   }
   return cuda_check(cudaGetLastError(), "decay states launch");
 }
 
-// behind_scan: the launch before is this call's scan, whose prefix the kernel waits for.
-int launch_decay_rows(const Pass& p, rehyat_dtype dt, bool out_f32, bool behind_scan,
-                      cudaStream_t st) {
-  const dim3 grid(p.nseg, p.B * p.H);
+// behind_scan: the launch before is this call's scan, whose prefixes the kernel waits for.
+int launch_decay_rows(const Pass* p, int n, rehyat_dtype dt, bool behind_scan, cudaStream_t st) {
+  const dim3 grid(p[0].nseg, p[0].B * p[0].H, n);
   if (dt == REHYAT_F32) {
     using namespace rehyat::decay;
-    const int smem = rows_smem_floats(padded(p.D)) * 4;
-    RH_TRY(cuda_check(cudaFuncSetAttribute(decay_rows_kernel,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
-                      "decay rows attr"));
-    decay_rows_kernel<<<grid, kThreads, smem, st>>>(p);
-    return cuda_check(cudaGetLastError(), "decay rows launch");
+    Passes a{};
+    for (int i = 0; i < n; ++i) a.p[i] = p[i];
+    const int smem = rows_smem_floats(padded(p[0].D)) * 4;
+    RH_TRY(allow_smem<decay_rows_kernel>(rows_smem_floats(kMaxD) * 4));
+    Behind l(grid, kThreads, smem, st, behind_scan);
+    return cuda_check(cudaLaunchKernelEx(&l.cfg, decay_rows_kernel, a), "decay rows launch");
   }
   using namespace rehyat::decay::tc;
-  CUtensorMap ma, mb, mc, mo;
-  RH_TRY(map_of(&ma, p.a, p));
-  RH_TRY(map_of(&mb, p.b, p));
-  RH_TRY(map_of(&mc, p.c, p));
-  mo = ma;  // unused with fp32 output
-  if (!out_f32) RH_TRY(make_map_rows(&mo, Rows{p.out, p.ob, p.oh, p.on, 1}, p.D, p.N, p.H, p.B));
-  auto k = p.reverse ? (out_f32 ? decay_rows_bf16_kernel<true, true> : decay_rows_bf16_kernel<true, false>)
-                     : decay_rows_bf16_kernel<false, false>;
-  RH_TRY(cuda_check(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRwSmem),
-                    "decay rows attr"));
+  RowsArgs a{};
+  for (int i = 0; i < n; ++i) {
+    a.p[i] = p[i];
+    RH_TRY(map_of(&a.a[i], p[i].a, p[i]));
+    RH_TRY(map_of(&a.b[i], p[i].b, p[i]));
+    RH_TRY(map_of(&a.c[i], p[i].c, p[i]));
+    a.out[i] = a.a[i];  // unused with fp32 output
+    if (!p[i].out_f32)
+      RH_TRY(make_map_rows(&a.out[i], Rows{p[i].out, p[i].ob, p[i].oh, p[i].on, 1}, p[i].D, p[i].N,
+                           p[i].H, p[i].B));
+  }
+  RH_TRY(allow_smem<decay_rows_bf16_kernel>(kRwSmem));
   Behind l(grid, kRwThreads, kRwSmem, st, behind_scan);
-  return cuda_check(cudaLaunchKernelEx(&l.cfg, k, ma, mb, mc, mo, p), "decay rows launch");
+  return cuda_check(cudaLaunchKernelEx(&l.cfg, decay_rows_bf16_kernel, a), "decay rows launch");
 }
 
-int launch_decay_scan(const Pass& p, const float* S0, float* last, bool need_prefix,
-                      bool behind_states, cudaStream_t st) {
-  const int n4 = p.D * p.D / 4;
-  Behind l(dim3((n4 + 255) / 256, p.B * p.H), 256, 0, st, behind_states);
-  return cuda_check(cudaLaunchKernelEx(&l.cfg, rehyat::decay::decay_scan_kernel, p.delta, S0, last,
-                                       p.log_decay, p.lengths, p.H, p.N, p.D, p.nseg, p.seg_rows,
-                                       p.reverse, (int)need_prefix),
+// The state before every segment of n <= 2 passes (rows b, c; time direction and e as in each) from
+// S0[i] (or zero), and the state after the last into last[i] unless null.  Sets each pass's prefix,
+// null for zero.  *scanned: whether a scan was launched.
+int decay_prefixes(Pass* p, int n, rehyat_dtype dt, const float* const* S0, float* const* last,
+                   bool* scanned, cudaStream_t st) {
+  const bool many = p[0].nseg > 1;
+  Pass need[2];
+  rehyat::decay::Scans a{};
+  int sums = 0, scans = 0;
+  for (int i = 0; i < n; ++i) {
+    const bool carried = many || S0[i];
+    p[i].prefix = carried ? p[i].delta : nullptr;
+    p[i].exact = last[i] != nullptr;
+    p[i].seg_skip = last[i] ? -1 : (p[i].reverse ? 0 : p[i].nseg - 1);
+    if (many || last[i]) need[sums++] = p[i];
+    if (carried || last[i])
+      a.s[scans++] = rehyat::decay::Scan{p[i].delta, S0[i], last[i], p[i].reverse, carried};
+  }
+  *scanned = scans > 0;
+  if (scans == 0) return REHYAT_OK;
+  const bool summed = sums > 0 && p[0].N > 0;
+  if (summed) RH_TRY(launch_decay_states(need, sums, dt, st));
+  a.log_decay = p[0].log_decay; a.lengths = p[0].lengths;
+  a.H = p[0].H; a.N = p[0].N; a.D = p[0].D; a.nseg = p[0].nseg; a.seg_rows = p[0].seg_rows;
+  const int n4 = a.D * a.D / 4;
+  Behind l(dim3((n4 + 255) / 256, p[0].B * p[0].H, scans), 256, 0, st, summed);
+  return cuda_check(cudaLaunchKernelEx(&l.cfg, rehyat::decay::decay_scan_kernel, a),
                     "decay scan launch");
-}
-
-// The state before every segment of a pass (rows b, c; time direction and e as in `p`) from `S0`
-// (or zero), and the state after the last into `last` unless null.  *prefix: where the row pass
-// reads it ([B*H][nseg][D][D]), null for zero.  *scanned: whether a scan was launched for them.
-int decay_prefix(Pass p, rehyat_dtype dt, const float* S0, float* last, const float** prefix,
-                 bool* scanned, cudaStream_t st) {
-  const bool many = p.nseg > 1, bf16 = dt == REHYAT_BF16;
-  *prefix = nullptr;
-  *scanned = false;
-  if (!many && !last) {
-    *prefix = S0;
-    return REHYAT_OK;
-  }
-  if (p.N > 0) {
-    p.seg_skip = last ? -1 : (p.reverse ? 0 : p.nseg - 1);
-    RH_TRY(launch_decay_states(p, dt, last != nullptr, st));
-  }
-  // the row pass reads the workspace's copy of S0, since `last` may be S0
-  RH_TRY(launch_decay_scan(p, S0, last, many || S0, bf16 && p.N > 0, st));
-  if (many || S0) *prefix = p.delta;
-  *scanned = true;
-  return REHYAT_OK;
 }
 
 Pass decay_pass(const DecayDims& a, const float* log_decay, const int* lengths,
@@ -368,10 +384,10 @@ int rehyat_decay_forward(const rehyat_decay_forward_args* args, void* stream) {
   p.sp = p.si = a.scale;
   p.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + pl.fwd);
   bool scanned;
-  RH_TRY(decay_prefix(p, d.dt, a.S0, a.S_last, &p.prefix, &scanned, st));
+  RH_TRY(decay_prefixes(&p, 1, d.dt, &a.S0, &a.S_last, &scanned, st));
   if (a.N == 0) return REHYAT_OK;
   set_out(p, a.out);
-  return launch_decay_rows(p, d.dt, false, scanned, st);
+  return launch_decay_rows(&p, 1, d.dt, scanned, st);
 }
 
 int rehyat_decay_backward(const rehyat_decay_backward_args* args, void* stream) {
@@ -399,62 +415,60 @@ int rehyat_decay_backward(const rehyat_decay_backward_args* args, void* stream) 
   const Rows rq = rows_of(a.q, 1), rk = rows_of(a.k, group), rv = rows_of(a.v, group),
              rdo = rows_of(a.dout, 1);
 
-  // dQ: forward in time over the states of the prompt, transposed
-  Pass f = decay_pass(d, a.log_decay, a.lengths, pl.seg);
-  f.delta = reinterpret_cast<float*>(ws + pl.fwd);
-  f.e = 1;
-  bool scanned = false;
-  if (a.N > 0) {
-    f.b = rk;
-    f.c = rv;
-    RH_TRY(decay_prefix(f, d.dt, a.S0, nullptr, &f.prefix, &scanned, st));
-    f.a = rdo;
-    f.b = rv;
-    f.c = rk;
-    f.transposed = 1;
-    f.sp = f.si = a.scale;
-    set_out(f, a.dq);
-    RH_TRY(launch_decay_rows(f, d.dt, false, scanned, st));
-  }
-
-  // dK, dV: backward in time over the gradient of the state, sum of scale * q dO^T
-  Pass r = decay_pass(d, a.log_decay, a.lengths, pl.seg);
-  r.delta = reinterpret_cast<float*>(ws + pl.bwd);
-  r.reverse = 1;
-  r.e = 0;
-  r.b = rq;
-  r.c = rdo;
-  r.sp = r.sd = a.scale;
-  RH_TRY(decay_prefix(r, d.dt, a.dS_last, a.dS0, &r.prefix, &scanned, st));
+  // states of the prompt, forward in time, for dQ (read transposed); gradient of the state, sum of
+  // scale * q dO^T backward in time, for dK (transposed) and dV
+  Pass s[2] = {decay_pass(d, a.log_decay, a.lengths, pl.seg),
+               decay_pass(d, a.log_decay, a.lengths, pl.seg)};
+  s[0].delta = reinterpret_cast<float*>(ws + pl.fwd);
+  s[0].e = 1;
+  s[0].b = rk;
+  s[0].c = rv;
+  s[0].sp = s[0].si = a.scale;
+  s[1].delta = reinterpret_cast<float*>(ws + pl.bwd);
+  s[1].reverse = 1;
+  s[1].b = rq;
+  s[1].c = rdo;
+  s[1].sp = s[1].sd = a.scale;
+  const float* first[2] = {a.S0, a.dS_last};
+  float* last[2] = {nullptr, a.dS0};
+  bool scanned;
+  RH_TRY(decay_prefixes(s, 2, d.dt, first, last, &scanned, st));
   if (a.N == 0) return REHYAT_OK;
-  float* part = reinterpret_cast<float*>(ws + pl.part);
-  for (int i = 0; i < 2; ++i) {
-    Pass p = r;
-    p.a = i ? rk : rv;
-    p.b = i ? rq : rdo;
-    p.c = i ? rdo : rq;
-    p.transposed = i ? 0 : 1;
-    const rehyat_rows& dst = i ? a.dv : a.dk;
-    if (group == 1) {
-      set_out(p, dst);
-      RH_TRY(launch_decay_rows(p, d.dt, false, scanned && i == 0, st));
-      continue;
-    }
-    const long long head = (long long)a.N * a.D;
-    set_out(p, rehyat_rows{part, head * a.H, head, a.D});
-    RH_TRY(launch_decay_rows(p, d.dt, true, scanned && i == 0, st));
-    const long long vec = head / 4;
-    const dim3 grid((unsigned)(vec / 1024 + 1 < 4096 ? vec / 1024 + 1 : 4096), a.B * a.Hk);
-    if (d.dt == REHYAT_BF16)
-      rehyat::decay::decay_group_sum_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(
-          part, static_cast<__nv_bfloat16*>(dst.p), dst.batch, dst.head, dst.row, a.Hk, group, a.N,
-          a.D);
-    else
-      rehyat::decay::decay_group_sum_kernel<float><<<grid, 256, 0, st>>>(
-          part, static_cast<float*>(dst.p), dst.batch, dst.head, dst.row, a.Hk, group, a.N, a.D);
-    RH_TRY(cuda_check(cudaGetLastError(), "decay group sum launch"));
+  const bool shared = group > 1;
+  const long long head = (long long)a.N * a.D;
+  Pass p[3] = {s[0], s[1], s[1]};
+  p[0].a = rdo;
+  p[0].b = rv;
+  p[0].c = rk;
+  p[0].transposed = 1;
+  set_out(p[0], a.dq);
+  p[1].a = rv;
+  p[1].b = rdo;
+  p[1].c = rq;
+  p[1].transposed = 1;
+  p[2].a = rk;
+  for (int i = 1; i < 3; ++i) {
+    p[i].out_f32 = shared;
+    set_out(p[i], shared ? rehyat_rows{ws + pl.part[i - 1], head * a.H, head, a.D}
+                         : (i == 1 ? a.dk : a.dv));
   }
-  return REHYAT_OK;
+  RH_TRY(launch_decay_rows(p, 3, d.dt, scanned, st));
+  if (!shared) return REHYAT_OK;
+  rehyat::decay::GroupSum g{};
+  for (int i = 0; i < 2; ++i) {
+    const rehyat_rows& o = i ? a.dv : a.dk;
+    g.part[i] = reinterpret_cast<const float*>(ws + pl.part[i]);
+    g.out[i] = o.p;
+    g.ob[i] = o.batch; g.oh[i] = o.head; g.on[i] = o.row;
+  }
+  g.Hk = a.Hk; g.group = group; g.N = a.N; g.D = a.D;
+  const long long blocks = head / 4 / 1024 + 1;
+  const dim3 grid((unsigned)(blocks < 4096 ? blocks : 4096), a.B * a.Hk, 2);
+  if (d.dt == REHYAT_BF16)
+    rehyat::decay::decay_group_sum_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(g);
+  else
+    rehyat::decay::decay_group_sum_kernel<float><<<grid, 256, 0, st>>>(g);
+  return cuda_check(cudaGetLastError(), "decay group sum launch");
 }
 
 int rehyat_decay_step(const rehyat_decay_step_args* args, void* stream) {

@@ -100,7 +100,7 @@ def test_argument_blocks_match_the_header(lib):
 def test_workspace_grows_with_shared_heads_only_for_gradients(lib):
     size = lambda Hk, bwd: rb.decay_workspace_size(1, 4, Hk, 1000, 64, bwd)  # noqa: E731
     assert size(4, False) == size(2, False)
-    assert size(2, True) - size(4, True) == 4 * 1000 * 64 * 4
+    assert size(2, True) - size(4, True) == 2 * 4 * 1000 * 64 * 4  # dk and dv of every query head
     assert rb.decay_workspace_size(1, 4, 4, 0, 64) > 0
     with pytest.raises(rb.RehyatError):
         rb.decay_workspace_size(1, 4, 3, 10, 64)
