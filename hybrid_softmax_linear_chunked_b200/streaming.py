@@ -14,6 +14,8 @@ chunk and its own overlap (`To`) and the next step's (`To_next`): a variable sch
 The session's state is its checkpoint: S, Z, the carry and the number of frames seen.
 state_dict() copies it to host memory; load_state_dict() puts it back into a fresh session, and
 the steps that follow produce the same bits as an uninterrupted run (same kernels, same order).
+
+DecayStream is the same for the pure recurrent layer (linear attention with a decay per head).
 """
 from __future__ import annotations
 
@@ -85,3 +87,85 @@ class ChunkStream:
         self.k_carry.copy_(st["k_carry"])
         self.v_carry.copy_(st["v_carry"])
         self.frames_seen = int(st["frames_seen"])
+
+
+class DecayStream:
+    """Decayed linear attention as a session: prompts of any length, then one token at a time, each
+    going on from the states the calls before left (decay_forward and decay_step of the binding),
+    with rotary positions on q and k counted per sequence.
+
+    The session owns the states [B,H,D,D] fp32, the number of rows each sequence has seen ([B]
+    int32 on the device, so ragged prompts and captured steps need no host value) and a workspace
+    that grows with the longest prompt.  Memory does not grow with the rows seen.
+
+    log_decay [H] fp32; Hk key/value heads (default H); scale defaults to D ** -0.5.  freq (fp64
+    [R/2], see rotary_frequencies) turns on rotary positions; rotary_scale and interleaved as in
+    `rotary`.  state_dict() / load_state_dict() checkpoint it: the calls that follow a resume
+    produce the same bits as an uninterrupted run."""
+
+    def __init__(self, log_decay, *, B: int, D: int, Hk: int | None = None,
+                 scale: float | None = None, freq: torch.Tensor | None = None,
+                 rotary_scale: float = 1.0, interleaved: bool = False):
+        self.log_decay, self.freq = log_decay, freq
+        self.B, self.H, self.D = B, log_decay.shape[0], D
+        self.Hk = self.H if Hk is None else Hk
+        self.scale = D ** -0.5 if scale is None else scale
+        self.rotary_scale, self.interleaved = rotary_scale, interleaved
+        dev = log_decay.device
+        self.state = torch.zeros(B, self.H, D, D, dtype=torch.float32, device=dev)
+        self.seen = torch.zeros(B, dtype=torch.int32, device=dev)
+        self.workspace = None
+
+    def reset(self) -> None:
+        """Start new sequences (the buffers are kept)."""
+        self.state.zero_()
+        self.seen.zero_()
+
+    def _check(self, q, k, v) -> None:
+        B, H, Hk, D = self.B, self.H, self.Hk, self.D
+        n = q.shape[2] if q.dim() == 4 else 0
+        if tuple(q.shape) != (B, H, n, D) or tuple(k.shape) != (B, Hk, n, D) or v.shape != k.shape:
+            raise ValueError(f"q, k, v must be [{B},{H},n,{D}], [{B},{Hk},n,{D}] and the same, got "
+                             f"{tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
+
+    def _turn(self, q, k):
+        if self.freq is None:
+            return q, k
+        return rb.rotary(q, k, self.freq, start=self.seen, scale=self.rotary_scale,
+                         interleaved=self.interleaved)
+
+    def prompt(self, q, k, v, lengths: torch.Tensor | None = None) -> torch.Tensor:
+        """Outputs [B,H,N,D] of the next N rows of every sequence, or of the first lengths[b]
+        (int32 [B] on the device, 0 .. N) of a padded batch, whose other rows are zero."""
+        self._check(q, k, v)
+        B, H, N, D = q.shape
+        need = rb.decay_workspace_size(B, H, self.Hk, N, D)
+        if self.workspace is None or self.workspace.numel() < need:
+            self.workspace = torch.empty(need, dtype=torch.uint8, device=self.state.device)
+        q, k = self._turn(q, k)
+        out, _ = rb.decay_forward(q, k, v, self.log_decay, scale=self.scale, lengths=lengths,
+                                  state=self.state, final_state=self.state,
+                                  workspace=self.workspace)
+        self.seen += N if lengths is None else lengths.clamp(0, N)
+        return out
+
+    def step(self, q, k, v) -> torch.Tensor:
+        """Outputs [B,H,1,D] of the next token of every sequence."""
+        self._check(q, k, v)
+        q, k = self._turn(q, k)
+        out = rb.decay_step(q, k, v, self.log_decay, self.state, scale=self.scale)
+        self.seen += 1
+        return out
+
+    def _shape(self):
+        return (self.B, self.H, self.Hk, self.D)
+
+    def state_dict(self) -> dict:
+        """The session's state, copied to host memory."""
+        return {"state": self.state.cpu(), "seen": self.seen.cpu(), "shape": self._shape()}
+
+    def load_state_dict(self, st: dict) -> None:
+        if tuple(st["shape"]) != self._shape():
+            raise ValueError(f"state of shape {st['shape']} does not fit this session")
+        self.state.copy_(st["state"])
+        self.seen.copy_(st["seen"])
