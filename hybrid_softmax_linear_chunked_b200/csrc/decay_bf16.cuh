@@ -290,7 +290,7 @@ constexpr int kRwIn = 16, kRwMma = 17, kRwOut = 18;
 constexpr uint32_t kRwStage = 3 * kTile;
 constexpr uint32_t kRwOffS = 2 * kRwStage;
 constexpr uint32_t kRwSmem = kRwOffS + kTile + 1024;
-static_assert(kRwSmem + 512 <= 232448, "shared memory over the limit");
+static_assert(kRwSmem + 2048 <= 232448 + 512, "shared memory over the limit");
 // TMEM columns: scores a b^T (P over them), P c, a S, the chunk's own b^T c
 constexpr uint32_t kColP = 0, kColIn = 128, kColSt = 256, kColAdd = 384;
 
@@ -336,7 +336,12 @@ __device__ __forceinline__ void rows_of_segment(const CUtensorMap& tmA, const CU
   __shared__ __align__(8) uint64_t bars[kNum];
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
+  __shared__ float diag_sh[64];  // sp L^(i - 31), zeros below 31: the past of a 32 x 32 block
   volatile int* abort_flag = &abort_sh;
+  if (tid < 64) {
+    const float g2 = log2_decay(p.log_decay, h);
+    diag_sh[tid] = tid < 31 ? 0.f : p.sp * ex2(g2 * (float)(tid - 31));
+  }
   if (warp == kRwIn) {
     tmem_alloc(&tmem_sh, 512);
     tmem_relinquish();
@@ -505,7 +510,16 @@ __device__ __forceinline__ void rows_of_segment(const CUtensorMap& tmA, const CU
         } else {
           uint32_t v[32];
           tmem_ld32(tmem + lanes + kColP + jb * 32, v);
-          if (jb == rw || (kReverse && rows < kRows)) {
+          if (rows == kRows && jb == rw) {
+            // the powers of the diagonal block by lane - column; above it they are zeros
+            const float* w = diag_sh + (kReverse ? 31 - lane : lane + 31);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              pk[j] = f2_bf16(f2_mul(f2_pack(w[kReverse ? 2 * j : -2 * j],
+                                             w[kReverse ? 2 * j + 1 : -2 * j - 1]),
+                                     f2_bits(v[2 * j], v[2 * j + 1])));
+          } else if (jb == rw || (kReverse && rows < kRows)) {
+            // a chunk with padding, whose scores may hold anything: one power and mask an element
             const int d0 = kReverse ? jb * 32 - r : r - jb * 32;
             const int stop = rows - jb * 32;
 #pragma unroll
