@@ -18,7 +18,7 @@
 // so that the kernels' threads, one row each, read and write neighbouring float4s (by rows, a state
 // took a row-pass CTA 3.8 us to read and a states CTA 2.9 us to write).
 //
-// A sequence is cut into segments of whole 128-row blocks.  Three launches: the sum of every
+// A sequence is cut into segments of whole chunks.  Three launches: the sum of every
 // segment's own rows (decay_states), its exclusive prefix in time order (decay_scan), and the rows
 // of every segment, chunk after chunk with the state carried along (decay_rows).  Every exponent
 // above is >= 0, so no power grows for L <= 1 and none is divided by; L = 0 (log_decay = -inf)
@@ -36,7 +36,6 @@ namespace rehyat {
 namespace decay {
 
 constexpr int kMaxD = 128;
-constexpr int kBlockRows = 128;  // segments start at multiples of this
 constexpr int kC = 64;           // rows of one chunk of the CUDA-core kernels
 constexpr int kThreads = 256;
 
@@ -105,110 +104,107 @@ __device__ __forceinline__ float4 mul4(float s, float4 v) {
   return make_float4(s * v.x, s * v.y, s * v.z, s * v.w);
 }
 
-// Rows [r0, r0 + kC) of one head into shared memory as fp32 [kC][ld], columns [D, Dp) and rows at
-// or past `end` as zeros whatever the tensor holds there.
-__device__ __forceinline__ void load_rows(float* dst, int ld, const Rows& t, int b, int h, int r0,
-                                          int end, int D, int Dp) {
-  const float* src = static_cast<const float*>(t.p) + b * t.sb + (h / t.group) * t.sh;
-  const int v4 = Dp / 4;
-  for (int i = threadIdx.x; i < kC * v4; i += kThreads) {
-    const int r = i / v4, c = (i - r * v4) * 4;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r0 + r < end && c < D) x = load4<float>(src + (long long)(r0 + r) * t.sn + c);
-    *reinterpret_cast<float4*>(dst + r * ld + c) = x;
-  }
-}
-
-// Shared memory of the CUDA-core kernels in floats: tiles have rows of Dp + 4 (Dp = D rounded up
-// to 32), so that threads of a warp on different rows reach different banks.
+// ---- fp32 rows on the CUDA cores ----
+// kDp: D rounded up to 32, with n = kDp / 32.  256 threads form 16 x 16 groups; a thread's columns are
+// the pairs 2 (tid % 16) + 32 u, u < n, so a half warp's eight-byte reads are one 128-byte row, and
+// products are taken two columns at a time.  Tiles have rows of kDp + 4, so that threads on different
+// rows reach different banks.
 __host__ __device__ constexpr int padded(int D) { return (D + 31) / 32 * 32; }
 __host__ __device__ constexpr int rows_smem_floats(int Dp) {
-  return 3 * kC * (Dp + 4) + kC * (kC + 4) + Dp * (Dp + 4);
+  return 3 * kC * (Dp + 4) + kC * (kC + 4) + Dp * (Dp + 4) + 2 * kC;
 }
-__host__ __device__ constexpr int states_smem_floats(int Dp) { return 2 * kC * (Dp + 4); }
+__host__ __device__ constexpr int states_smem_floats(int Dp) { return 2 * kC * (Dp + 4) + kC; }
 
-// acc[8][8] += sum_r (w[r] x[r][i0 + 8]) y[r][j0 + 8]^T over the kC rows of two tiles; the thread's
-// rows are i0 .. i0+3, i0+64 .. (half apart) and columns likewise, so a warp's float4 reads fall
-// on neighbouring banks.
-struct Outer {
-  int i0, j0, half;
-  bool on;
-};
-__device__ __forceinline__ Outer outer_of(int Dp) {
-  // (Dp / 8)^2 threads hold 8 x 8 elements each
-  const int n = Dp / 8;
-  Outer o;
-  o.on = threadIdx.x < n * n;
-  o.i0 = (threadIdx.x / n) * 4;
-  o.j0 = (threadIdx.x % n) * 4;
-  o.half = Dp / 2;
-  return o;
+__device__ __forceinline__ uint64_t pair_at(const float* p) {
+  return *reinterpret_cast<const uint64_t*>(p);
 }
-__device__ __forceinline__ void outer_add(float4 (&acc)[8][2], const float* x, const float* y,
-                                          int ld, const Outer& o, float g2, int last_time,
-                                          int first_row, int sign, float sd, int rows) {
-  // weight of row r: sd * L^(last_time - sign * (first_row + r))
-#pragma unroll 2
-  for (int r = 0; r < rows; ++r) {
-    const float w = sd * exp2f(g2 * (float)(last_time - sign * (first_row + r)));
-    const float4 x0 = *reinterpret_cast<const float4*>(x + r * ld + o.i0);
-    const float4 x1 = *reinterpret_cast<const float4*>(x + r * ld + o.i0 + o.half);
-    const float4 y0 = mul4(w, *reinterpret_cast<const float4*>(y + r * ld + o.j0));
-    const float4 y1 = mul4(w, *reinterpret_cast<const float4*>(y + r * ld + o.j0 + o.half));
-    const float xs[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+__device__ __forceinline__ uint64_t twice(float x) { return sm100::f2_pack(x, x); }
+
+// Rows [r0, r0 + kC) of one head into shared memory, columns [D, kDp) and rows at or past `end` as
+// zeros whatever the tensor holds there.
+template <int kDp>
+__device__ __forceinline__ void load_rows(float* dst, const Rows& t, int b, int h, int r0, int end,
+                                          int D) {
+  const float* src = static_cast<const float*>(t.p) + b * t.sb + (h / t.group) * t.sh;
+  constexpr int v4 = kDp / 4;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      acc[i][0] = fma4(xs[i], y0, acc[i][0]);
-      acc[i][1] = fma4(xs[i], y1, acc[i][1]);
-    }
+  for (int i0 = 0; i0 < kC * v4; i0 += kThreads) {
+    const int i = i0 + threadIdx.x, r = i / v4, c = (i % v4) * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r0 + r < end && c < D) x = load4<float>(src + (long long)(r0 + r) * t.sn + c);
+    *reinterpret_cast<float4*>(dst + r * (kDp + 4) + c) = x;
   }
 }
-__device__ __forceinline__ int outer_row(const Outer& o, int i) {
-  return i < 4 ? o.i0 + i : o.i0 + o.half + i - 4;
+
+// acc += sum over `rows` rows r of (w[r] x[r][i]) y[r][j] for the thread's 2n x 2n elements: rows
+// i = 2 (tid / 16) + 32 u and the one after, columns likewise by tid % 16.
+template <int kDp>
+__device__ __forceinline__ void outer_add(uint64_t (&acc)[kDp / 16][kDp / 32], const float* x,
+                                          const float* y, const float* w, int rows) {
+  constexpr int n = kDp / 32, ld = kDp + 4;
+  const int i0 = (threadIdx.x / 16) * 2, j0 = (threadIdx.x % 16) * 2;
+#pragma unroll 2
+  for (int r = 0; r < rows; ++r) {
+    const uint64_t wr = twice(w[r]);
+    uint64_t yv[n];
+#pragma unroll
+    for (int u = 0; u < n; ++u) yv[u] = sm100::f2_mul(wr, pair_at(y + r * ld + j0 + 32 * u));
+#pragma unroll
+    for (int u = 0; u < n; ++u) {
+      const float2 xv = *reinterpret_cast<const float2*>(x + r * ld + i0 + 32 * u);
+#pragma unroll
+      for (int v = 0; v < n; ++v) {
+        acc[2 * u][v] = sm100::f2_fma(twice(xv.x), yv[v], acc[2 * u][v]);
+        acc[2 * u + 1][v] = sm100::f2_fma(twice(xv.y), yv[v], acc[2 * u + 1][v]);
+      }
+    }
+  }
 }
 
 // Each segment's own sum: delta = sd * sum_j L^(n - t_j - e) b_j c_j^T over its n valid rows.
 // grid (nseg, B*H, n), block 256.
-__global__ void __launch_bounds__(kThreads, 1)
+template <int kDp>
+__global__ void __launch_bounds__(kThreads, kDp <= 64 ? 2 : 1)
     decay_states_kernel(const __grid_constant__ Passes all) {
   extern __shared__ __align__(16) float smf[];
   sm100::grid_dep_signal();
   const Pass& p = all.p[blockIdx.z];
   const int seg = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh - b * p.H;
   if (seg == p.seg_skip) return;
-  const int Dp = padded(p.D), ld = Dp + 4;
+  constexpr int n = kDp / 32, ld = kDp + 4;
+  const int tid = threadIdx.x;
   float* sb = smf;
   float* sc = sb + kC * ld;
+  float* sw = sc + kC * ld;
   const float g2 = log2_decay(p.log_decay, h);
   const int r_begin = seg * p.seg_rows;
   const int r_end = min(r_begin + p.seg_rows, length_of(p.lengths, b, p.N));
-  const Outer o = outer_of(Dp);
-  float4 acc[8][2];
+  uint64_t acc[2 * n][n];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < 2 * n; ++i)
+#pragma unroll
+    for (int v = 0; v < n; ++v) acc[i][v] = 0ull;
   for (int r0 = r_begin; r0 < r_end; r0 += kC) {
     __syncthreads();
-    load_rows(sb, ld, p.b, b, h, r0, r_end, p.D, Dp);
-    load_rows(sc, ld, p.c, b, h, r0, r_end, p.D, Dp);
-    __syncthreads();
-    const int rows = min(kC, r_end - r0);
-    if (o.on) {
-      // forward: exponent r_end - 1 - r + (1 - e); backward: r - r_begin + (1 - e)
-      if (p.reverse)
-        outer_add(acc, sb, sc, ld, o, g2, 1 - p.e - r_begin, r0, -1, p.sd, rows);
-      else
-        outer_add(acc, sb, sc, ld, o, g2, r_end - p.e, r0, 1, p.sd, rows);
+    load_rows<kDp>(sb, p.b, b, h, r0, r_end, p.D);
+    load_rows<kDp>(sc, p.c, b, h, r0, r_end, p.D);
+    if (tid < kC) {
+      const int r = r0 + tid;
+      sw[tid] = p.sd * exp2f(g2 * (float)(p.reverse ? r - r_begin + 1 - p.e : r_end - p.e - r));
     }
+    __syncthreads();
+    outer_add<kDp>(acc, sb, sc, sw, min(kC, r_end - r0));
   }
-  if (!o.on) return;
   float* dst = p.delta + ((size_t)bh * p.nseg + seg) * p.D * p.D;
+  const int i0 = (tid / 16) * 2, j0 = (tid % 16) * 2;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = outer_row(o, i);
-    if (r >= p.D) continue;
-    if (o.j0 < p.D) store4(dst + o.j0 * p.D + r * 4, acc[i][0]);
-    if (o.j0 + o.half < p.D) store4(dst + (o.j0 + o.half) * p.D + r * 4, acc[i][1]);
-  }
+  for (int i = 0; i < 2 * n; ++i)
+#pragma unroll
+    for (int v = 0; v < n; ++v) {
+      const int r = i0 + 32 * (i / 2) + (i & 1), c = j0 + 32 * v;
+      if (r < p.D && c < p.D)
+        *reinterpret_cast<uint64_t*>(dst + (c & ~3) * p.D + r * 4 + (c & 3)) = acc[i][v];
+    }
 }
 
 // The state before each segment in time order, written over the segment's own sum, and the state
@@ -269,30 +265,34 @@ __global__ void __launch_bounds__(256) decay_scan_kernel(const __grid_constant__
   if (last) reinterpret_cast<float4*>(last)[(size_t)bh * n4 + at] = acc;
 }
 
-// The rows of one segment: chunks of kC in time order, the state [D][D] carried in shared memory.
-// Bound by the fp32 pipes: 2 kC D (kC + 2 D) multiply-adds a chunk.
+// The rows of one segment: chunks of kC in time order, the state carried in shared memory.
+// Bound by the fp32 pipes: kC D (kC + kC / 2 + 2 D) multiply-adds a chunk.
 // grid (nseg, B*H, n), block 256.
-__global__ void __launch_bounds__(kThreads, 1)
+template <int kDp>
+__global__ void __launch_bounds__(kThreads, kDp <= 64 ? 2 : 1)
     decay_rows_kernel(const __grid_constant__ Passes all) {
   extern __shared__ __align__(16) float smf[];
   const Pass& p = all.p[blockIdx.z];
   const int seg = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh - b * p.H;
-  const int Dp = padded(p.D), ld = Dp + 4, ldp = kC + 4;
+  constexpr int n = kDp / 32, ld = kDp + 4, ldp = kC + 4;
   float* sa = smf;
   float* sb = sa + kC * ld;
   float* sc = sb + kC * ld;
   float* sp = sc + kC * ld;
   float* ss = sp + kC * ldp;
-  const int tid = threadIdx.x;
+  float* spow = ss + kDp * ld;  // sp L^d
+  float* sw = spow + kC;        // weights of b's rows
+  const int tid = threadIdx.x, warp = tid >> 5;
   const float g2 = log2_decay(p.log_decay, h);
-  const int n = length_of(p.lengths, b, p.N);
+  const int len = length_of(p.lengths, b, p.N);
   const int r_begin = seg * p.seg_rows, r_stop = min(r_begin + p.seg_rows, p.N);
-  const int r_end = min(r_stop, n);
+  const int r_end = min(r_stop, len);
   float* out = static_cast<float*>(p.out) + b * p.ob + h * p.oh;
+  if (tid < kC) spow[tid] = p.sp * exp2f(g2 * (float)tid);
 
   sm100::grid_dep_wait();  // the prefix comes from the launch before
-  for (int i = tid; i < Dp * (Dp / 4); i += kThreads) {
-    const int r = i / (Dp / 4), c = (i - r * (Dp / 4)) * 4;
+  for (int i = tid; i < kDp * (kDp / 4); i += kThreads) {
+    const int r = i % kDp, c = (i / kDp) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (p.prefix && r < p.D && c < p.D) {
       const float* src = p.prefix + ((size_t)bh * p.nseg + seg) * p.D * p.D;
@@ -305,37 +305,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     *reinterpret_cast<float4*>(ss + r * ld + c) = x;
   }
-  const Outer o = outer_of(Dp);
   const int nc = (r_stop - r_begin + kC - 1) / kC;
-  const int v4 = Dp / 4;
-  // output tile: 16 groups of 4 rows x (Dp / 8) columns of 8 (as 4 + 4, half apart)
-  const int ncol = Dp / 8;
-  const bool o_on = tid < 16 * ncol;
-  const int orow = (tid / ncol) * 4, ocol = (tid % ncol) * 4, ohalf = Dp / 2;
+  const int i4 = (tid / 16) * 4, j2 = (tid % 16) * 2;  // rows i4 .. i4 + 3, column pairs from j2
   for (int ci = 0; ci < nc; ++ci) {
     const int r0 = r_begin + (p.reverse ? nc - 1 - ci : ci) * kC;
     const int rows = min(max(r_end - r0, 0), kC);  // valid rows
     __syncthreads();
     if (rows == 0) {  // nothing but padding: zeros, the state stays
-      for (int i = tid; i < kC * v4; i += kThreads) {
-        const int r = i / v4, c = (i - r * v4) * 4;
+      for (int i = tid; i < kC * (kDp / 4); i += kThreads) {
+        const int r = i / (kDp / 4), c = (i % (kDp / 4)) * 4;
         if (r0 + r < r_stop && c < p.D)
           store4(out + (long long)(r0 + r) * p.on + c, make_float4(0.f, 0.f, 0.f, 0.f));
       }
       continue;
     }
-    load_rows(sa, ld, p.a, b, h, r0, r_end, p.D, Dp);
-    load_rows(sb, ld, p.b, b, h, r0, r_end, p.D, Dp);
-    load_rows(sc, ld, p.c, b, h, r0, r_end, p.D, Dp);
+    load_rows<kDp>(sa, p.a, b, h, r0, r_end, p.D);
+    load_rows<kDp>(sb, p.b, b, h, r0, r_end, p.D);
+    load_rows<kDp>(sc, p.c, b, h, r0, r_end, p.D);
+    if (tid < kC)
+      sw[tid] = p.sd * exp2f(g2 * (float)(p.reverse ? tid + 1 - p.e : rows - p.e - tid));
     __syncthreads();
     {  // P = sp * L^|i-j| (a_i . b_j) over the past of i, 4 x 4 a thread (columns 16 apart)
-      const int i0 = (tid / 16) * 4, j0 = tid % 16;
+      const int j0 = tid % 16;
       float acc[4][4] = {};
-      for (int k = 0; k < Dp; k += 4) {
+#pragma unroll 4
+      for (int k = 0; k < kDp; k += 4) {
         float4 x[4], y[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          x[u] = *reinterpret_cast<const float4*>(sa + (i0 + u) * ld + k);
+          x[u] = *reinterpret_cast<const float4*>(sa + (i4 + u) * ld + k);
           y[u] = *reinterpret_cast<const float4*>(sb + (j0 + 16 * u) * ld + k);
         }
 #pragma unroll
@@ -349,86 +347,75 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = 0; u < 4; ++u)
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const int i = i0 + u, j = j0 + 16 * w;
-          const int d = p.reverse ? j - i : i - j;
-          sp[i * ldp + j] =
-              d >= 0 && j < rows ? p.sp * exp2f(g2 * (float)d) * acc[u][w] : 0.f;
+          const int i = i4 + u, j = j0 + 16 * w, d = p.reverse ? j - i : i - j;
+          sp[i * ldp + j] = d >= 0 && j < rows ? spow[max(d, 0)] * acc[u][w] : 0.f;
         }
     }
     __syncthreads();
-    if (o_on) {  // out = si * L^(t + e) a^T S + P c
-      float4 acc[4][2];
+    {  // out = si * L^(t + e) a^T S + P c
+      uint64_t acc[4][n];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) acc[u][0] = acc[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = 0; k < Dp; k += 4) {
-        float4 x[4];
+      for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const float4*>(sa + (orow + u) * ld + k);
+        for (int v = 0; v < n; ++v) acc[u][v] = 0ull;
+      auto add = [&](const float* xr, int ldx, const float* y, int k0, int k1) {
+#pragma unroll 2
+        for (int k = k0; k < k1; k += 4) {
+          float4 x[4];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const float4 y0 = *reinterpret_cast<const float4*>(ss + (k + w) * ld + ocol);
-          const float4 y1 = *reinterpret_cast<const float4*>(ss + (k + w) * ld + ocol + ohalf);
+          for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const float4*>(xr + (i4 + u) * ldx + k);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float xv = w == 0 ? x[u].x : w == 1 ? x[u].y : w == 2 ? x[u].z : x[u].w;
-            acc[u][0] = fma4(xv, y0, acc[u][0]);
-            acc[u][1] = fma4(xv, y1, acc[u][1]);
+          for (int w = 0; w < 4; ++w) {
+            uint64_t yv[n];
+#pragma unroll
+            for (int v = 0; v < n; ++v) yv[v] = pair_at(y + (k + w) * ld + j2 + 32 * v);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const float xv = w == 0 ? x[u].x : w == 1 ? x[u].y : w == 2 ? x[u].z : x[u].w;
+#pragma unroll
+              for (int v = 0; v < n; ++v) acc[u][v] = sm100::f2_fma(twice(xv), yv[v], acc[u][v]);
+            }
           }
         }
-      }
+      };
+      add(sa, ld, ss, 0, kDp);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int t = p.reverse ? rows - 1 - (orow + u) : orow + u;
-        const float f = p.si * exp2f(g2 * (float)(max(t, 0) + p.e));
-        acc[u][0] = mul4(f, acc[u][0]);
-        acc[u][1] = mul4(f, acc[u][1]);
+        const int t = p.reverse ? rows - 1 - (i4 + u) : i4 + u;
+        const uint64_t f = twice(p.si * exp2f(g2 * (float)(max(t, 0) + p.e)));
+#pragma unroll
+        for (int v = 0; v < n; ++v) acc[u][v] = sm100::f2_mul(f, acc[u][v]);
       }
-      for (int k = 0; k < kC; k += 4) {
-        float4 x[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const float4*>(sp + (orow + u) * ldp + k);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const float4 y0 = *reinterpret_cast<const float4*>(sc + (k + w) * ld + ocol);
-          const float4 y1 = *reinterpret_cast<const float4*>(sc + (k + w) * ld + ocol + ohalf);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float xv = w == 0 ? x[u].x : w == 1 ? x[u].y : w == 2 ? x[u].z : x[u].w;
-            acc[u][0] = fma4(xv, y0, acc[u][0]);
-            acc[u][1] = fma4(xv, y1, acc[u][1]);
-          }
-        }
-      }
+      // a warp's eight rows have no past beyond their last (first, backward in time)
+      add(sp, ldp, sc, p.reverse ? warp * 8 : 0, p.reverse ? kC : warp * 8 + 8);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int r = orow + u;
+        const int r = i4 + u;
         if (r0 + r >= r_stop) continue;
-        if (r >= rows) acc[u][0] = acc[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
         float* dst = out + (long long)(r0 + r) * p.on;
-        if (ocol < p.D) store4(dst + ocol, acc[u][0]);
-        if (ocol + ohalf < p.D) store4(dst + ocol + ohalf, acc[u][1]);
+#pragma unroll
+        for (int v = 0; v < n; ++v)
+          if (j2 + 32 * v < p.D)
+            *reinterpret_cast<uint64_t*>(dst + j2 + 32 * v) = r < rows ? acc[u][v] : 0ull;
       }
     }
     __syncthreads();
-    if (ci + 1 < nc && o.on) {  // S = L^rows S + sd * sum L^(rows - t - e) b c^T
-      const float keep = exp2f(g2 * (float)rows);
-      float4 acc[8][2];
+    if (ci + 1 < nc) {  // S = L^rows S + sd * sum L^(rows - t - e) b c^T
+      const uint64_t keep = twice(exp2f(g2 * (float)rows));
+      const int i2 = (tid / 16) * 2;
+      uint64_t acc[2 * n][n];
+      auto at = [&](int i, int v) {
+        return reinterpret_cast<uint64_t*>(ss + (i2 + 32 * (i / 2) + (i & 1)) * ld + j2 + 32 * v);
+      };
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float* s = ss + outer_row(o, i) * ld;
-        acc[i][0] = mul4(keep, *reinterpret_cast<const float4*>(s + o.j0));
-        acc[i][1] = mul4(keep, *reinterpret_cast<const float4*>(s + o.j0 + o.half));
-      }
-      if (p.reverse)
-        outer_add(acc, sb, sc, ld, o, g2, 1 - p.e, 0, -1, p.sd, rows);
-      else
-        outer_add(acc, sb, sc, ld, o, g2, rows - p.e, 0, 1, p.sd, rows);
+      for (int i = 0; i < 2 * n; ++i)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float* s = ss + outer_row(o, i) * ld;
-        *reinterpret_cast<float4*>(s + o.j0) = acc[i][0];
-        *reinterpret_cast<float4*>(s + o.j0 + o.half) = acc[i][1];
-      }
+        for (int v = 0; v < n; ++v) acc[i][v] = sm100::f2_mul(keep, *at(i, v));
+      outer_add<kDp>(acc, sb, sc, sw, rows);
+#pragma unroll
+      for (int i = 0; i < 2 * n; ++i)
+#pragma unroll
+        for (int v = 0; v < n; ++v) *at(i, v) = acc[i][v];
     }
   }
 }

@@ -62,25 +62,27 @@ Rows rows_of(const rehyat_rows& s, int group) {
 }
 
 // Segments of a sequence: one CTA each, so their number trades whole waves of the 148 SMs against
-// each CTA's start, which costs one to three chunks.  `blocks` of 128 rows.  A launch of three
-// passes takes the same cut: each pass fills the waves by itself (cut for all three at once, in one
-// wave of 64-chunk segments, the 480x832 5 s gradients took 380 us instead of 320).
+// each CTA's start, about one chunk of the bf16 kernels (128 rows) and a quarter of one of the fp32
+// kernels (64 rows).  A launch of three passes takes the same cut: each pass fills the waves by
+// itself (cut for all three at once, in one wave of 64-chunk segments, the 480x832 5 s gradients took
+// 380 us instead of 320).
 struct Segments {
   int n, rows;
 };
-Segments decay_segments(int BH, int N) {
-  const int blocks = (N + rehyat::decay::kBlockRows - 1) / rehyat::decay::kBlockRows;
-  Segments best{1, blocks > 0 ? blocks * rehyat::decay::kBlockRows : rehyat::decay::kBlockRows};
+Segments decay_segments(int BH, int N, rehyat_dtype dt) {
+  const int chunk = dt == REHYAT_BF16 ? rehyat::decay::tc::kRows : rehyat::decay::kC;
+  const int start = dt == REHYAT_BF16 ? 4 : 1;  // in quarters of a chunk
+  const int chunks = N > 0 ? (N + chunk - 1) / chunk : 1;
+  Segments best{1, chunks * chunk};
   long long best_cost = -1;
-  for (int n = 1; n <= blocks && n <= 256; ++n) {
-    const int per = (blocks + n - 1) / n;
-    const int used = (blocks + per - 1) / per;  // segments that hold rows
-    if (used != n) continue;
+  for (int n = 1; n <= chunks && n <= 256; ++n) {
+    const int per = (chunks + n - 1) / n;
+    if ((chunks + per - 1) / per != n) continue;  // the last ones would hold no rows
     const long long waves = ((long long)BH * n + 147) / 148;
-    const long long cost = waves * (per + 1);
+    const long long cost = waves * (4 * per + start);
     if (best_cost < 0 || cost < best_cost) {
       best_cost = cost;
-      best = Segments{n, per * rehyat::decay::kBlockRows};
+      best = Segments{n, per * chunk};
     }
   }
   return best;
@@ -93,7 +95,7 @@ struct DecayPlan {
 DecayPlan plan_decay(const DecayDims& a, bool backward) {
   DecayPlan p{};
   const size_t BH = (size_t)a.B * a.H;
-  p.seg = decay_segments((int)BH, a.N);
+  p.seg = decay_segments((int)BH, a.N, a.dt);
   Carve cv;
   const size_t states = BH * p.seg.n * a.D * a.D * 4;
   p.fwd = cv.take(states);
@@ -160,6 +162,23 @@ int allow_smem(int most) {
   return REHYAT_OK;
 }
 
+template <int kDp>
+int launch_f32_states(const rehyat::decay::Passes& a, dim3 grid, cudaStream_t st) {
+  using namespace rehyat::decay;
+  const int smem = states_smem_floats(kDp) * 4;
+  RH_TRY(allow_smem<decay_states_kernel<kDp>>(smem));
+  decay_states_kernel<kDp><<<grid, kThreads, smem, st>>>(a);
+  return REHYAT_OK;
+}
+template <int kDp>
+int launch_f32_rows(const rehyat::decay::Passes& a, dim3 grid, bool behind_scan, cudaStream_t st) {
+  using namespace rehyat::decay;
+  const int smem = rows_smem_floats(kDp) * 4;
+  RH_TRY(allow_smem<decay_rows_kernel<kDp>>(smem));
+  Behind l(grid, kThreads, smem, st, behind_scan);
+  return cuda_check(cudaLaunchKernelEx(&l.cfg, decay_rows_kernel<kDp>, a), "decay rows launch");
+}
+
 // The passes of one launch: the states they need, and the rows.
 int launch_decay_states(const Pass* p, int n, rehyat_dtype dt, cudaStream_t st) {
   const dim3 grid(p[0].nseg, p[0].B * p[0].H, n);
@@ -177,9 +196,12 @@ int launch_decay_states(const Pass* p, int n, rehyat_dtype dt, cudaStream_t st) 
     using namespace rehyat::decay;
     Passes a{};
     for (int i = 0; i < n; ++i) a.p[i] = p[i];
-    const int smem = states_smem_floats(padded(p[0].D)) * 4;
-    RH_TRY(allow_smem<decay_states_kernel>(states_smem_floats(kMaxD) * 4));
-    decay_states_kernel<<<grid, kThreads, smem, st>>>(a);
+    switch (padded(p[0].D)) {
+      case 32: RH_TRY(launch_f32_states<32>(a, grid, st)); break;
+      case 64: RH_TRY(launch_f32_states<64>(a, grid, st)); break;
+      case 96: RH_TRY(launch_f32_states<96>(a, grid, st)); break;
+      default: RH_TRY(launch_f32_states<128>(a, grid, st)); break;
+    }
   }
   return cuda_check(cudaGetLastError(), "decay states launch");
 }
@@ -191,10 +213,12 @@ int launch_decay_rows(const Pass* p, int n, rehyat_dtype dt, bool behind_scan, c
     using namespace rehyat::decay;
     Passes a{};
     for (int i = 0; i < n; ++i) a.p[i] = p[i];
-    const int smem = rows_smem_floats(padded(p[0].D)) * 4;
-    RH_TRY(allow_smem<decay_rows_kernel>(rows_smem_floats(kMaxD) * 4));
-    Behind l(grid, kThreads, smem, st, behind_scan);
-    return cuda_check(cudaLaunchKernelEx(&l.cfg, decay_rows_kernel, a), "decay rows launch");
+    switch (padded(p[0].D)) {
+      case 32: return launch_f32_rows<32>(a, grid, behind_scan, st);
+      case 64: return launch_f32_rows<64>(a, grid, behind_scan, st);
+      case 96: return launch_f32_rows<96>(a, grid, behind_scan, st);
+      default: return launch_f32_rows<128>(a, grid, behind_scan, st);
+    }
   }
   using namespace rehyat::decay::tc;
   RowsArgs a{};
@@ -352,10 +376,13 @@ int rehyat_rotary(const rehyat_rotary_args* args, void* stream) {
 
 int rehyat_decay_workspace_size(int B, int H, int Hk, int N, int D, int backward, size_t* bytes) {
   g_msg[0] = 0;
-  const DecayDims d{B, H, Hk, N, D, REHYAT_BF16, 1.f};
+  DecayDims d{B, H, Hk, N, D, REHYAT_BF16, 1.f};
   RH_TRY(check_decay(d));
   if (!bytes) return fail(REHYAT_ERR_ARG, "null pointer");
   *bytes = plan_decay(d, backward != 0).total;
+  d.dt = REHYAT_F32;
+  const size_t f32 = plan_decay(d, backward != 0).total;
+  if (f32 > *bytes) *bytes = f32;
   return REHYAT_OK;
 }
 
