@@ -650,40 +650,47 @@ def sync_status(device: torch.device | None = None) -> None:
 # These calls read tensors by their strides: [B, heads, N, D] with contiguous rows of D, so a
 # transposed [B, N, heads, D] projection or a slice of a packed qkv needs no copy.
 
-def _rows(t: torch.Tensor, like: torch.Tensor, shape, what: str):
-    """(pointer, strides of sequence, head and row) of a tensor of rows of this shape, of the type
-    and on the device of `like`."""
-    if t.dtype is not like.dtype or t.shape != shape or t.device != like.device:
-        _refuse(t, like.device, like.dtype, shape, what)
+# (a step is host-bound: these checks are a third of its time, so each compares once and leaves the
+# reason to _refuse)
+def _rows(t: torch.Tensor, dtype: torch.dtype, index: int, shape, what: str):
+    """(pointer, strides of sequence, head and row) of a tensor of rows of this type and shape on
+    CUDA device `index`."""
     b, h, n, d = t.stride()
-    if d != 1 and shape[3] > 1:
-        raise ValueError(f"{what}: the last dimension must be contiguous")
+    if d != 1 or t.dtype is not dtype or t.get_device() != index or t.shape != shape:
+        _refuse(t, dtype, index, shape, what)
+        if shape[3] > 1:
+            raise ValueError(f"{what}: the last dimension must be contiguous")
     return t.data_ptr(), b, h, n
 
 
-def _small(t: torch.Tensor | None, dev: torch.device, dtype: torch.dtype, shape, what: str) -> int:
-    """Pointer of an optional contiguous tensor of the given type and shape."""
-    if t is None:
-        return 0
-    if t.dtype is not dtype or t.shape != shape or t.device != dev:
-        _refuse(t, dev, dtype, shape, what)
-    if not t.is_contiguous():
+def _small(t: torch.Tensor, dtype: torch.dtype, index: int, shape, what: str) -> int:
+    """Pointer of a contiguous tensor of this type and shape."""
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or \
+            not t.is_contiguous():
+        _refuse(t, dtype, index, shape, what)
         raise ValueError(f"{what} must be contiguous")
     return t.data_ptr()
 
 
-def _refuse(t, dev, dtype, shape, what) -> None:
-    if t.device != dev:
+def _refuse(t, dtype, index, shape, what) -> None:
+    if t.get_device() != index:
         raise ValueError("all tensors must be on the same CUDA device")
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _cuda(dev: torch.device) -> torch.device:
-    if dev.type != "cuda":
-        raise ValueError("all tensors must be on the same CUDA device")
-    return dev
+def _typed(t: torch.Tensor):
+    """(dtype, its library code, device index) of the tensor that the others must match."""
+    dtype, index = t.dtype, t.get_device()
+    if dtype is torch.bfloat16:
+        code = REHYAT_BF16
+    elif dtype is torch.float32:
+        code = REHYAT_F32
+    else:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return dtype, code, index
 
 
 # (torch.cuda.current_stream builds a Stream object: 2 us of a step's 10)
@@ -698,22 +705,25 @@ def _scratch(nbytes: int, dev: torch.device, workspace: torch.Tensor | None) -> 
     return _workspace(nbytes, dev, workspace)
 
 
-def _call(dev: torch.device, fn, block: bytes) -> None:
-    """Enqueue a library call on the current stream of the tensors' device, whichever device is
-    the current one."""
-    if torch.cuda.current_device() == dev.index:
-        status = fn(block, _raw_stream(dev.index))
+def _call(index: int, fn, block: bytes) -> None:
+    """Enqueue a library call on the current stream of CUDA device `index`, whichever device is the
+    current one."""
+    if index < 0:
+        raise ValueError("all tensors must be on the same CUDA device")
+    if torch.cuda.current_device() == index:
+        status = fn(block, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            status = fn(block, _raw_stream(dev.index))
+        with torch.cuda.device(index):
+            status = fn(block, _raw_stream(index))
     if status:
         _check(status)
 
 
 def _four(t: torch.Tensor, what: str):
-    if t.dim() != 4:
-        raise ValueError(f"{what} must be [B, heads, N, D], got {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 4:
+        raise ValueError(f"{what} must be [B, heads, N, D], got {tuple(shape)}")
+    return shape
 
 
 def rotary_frequencies(R: int, *, base: float = 10000.0, scaling: str | None = None,
@@ -789,10 +799,10 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, freq: torch.Tensor, *,
     q_out, or (q_out, k_out); they may be q and k (in place)."""
     lib = _lib or load()
     B, H, n, D = shape = _four(q, "q")
-    dev, code = q.device, _dtype_code(q)
-    qa = _rows(q, q, shape, "q")
-    R = 2 * freq.numel()
-    fp = _small(freq, _cuda(dev), torch.float64, (R // 2,), "freq")
+    dtype, code, index = _typed(q)
+    qa = _rows(q, dtype, index, shape, "q")
+    half = freq.numel()
+    fp = _small(freq, torch.float64, index, (half,), "freq")
     pos, axes, add, pa, pb, pn = positions, 1, 0, 0, 0, 0
     if isinstance(start, torch.Tensor):
         if positions is not None:
@@ -802,36 +812,35 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, freq: torch.Tensor, *,
         pos, pb, add, start = start, start.stride(0), 1, 0
     elif positions is None:
         add = 1
+    elif positions.shape == (B, n):
+        pb, pn = positions.stride()
+    elif positions.dim() == 3 and positions.shape[1:] == (B, n):
+        axes, (pa, pb, pn) = positions.shape[0], positions.stride()
     else:
-        st = positions.stride()
-        if positions.shape == (B, n):
-            pb, pn = st
-        elif positions.dim() == 3 and positions.shape[1:] == (B, n):
-            axes, (pa, pb, pn) = positions.shape[0], st
-        else:
-            raise ValueError(f"positions must have shape {(B, n)} or (axes, {B}, {n}), got "
-                             f"{tuple(positions.shape)}")
+        raise ValueError(f"positions must have shape {(B, n)} or (axes, {B}, {n}), got "
+                         f"{tuple(positions.shape)}")
     pp = pos64 = 0
     if pos is not None:
-        if pos.device != dev:
-            raise ValueError("all tensors must be on the same CUDA device")
-        if pos.dtype not in (torch.int32, torch.int64):
+        pos64 = pos.dtype is torch.int64
+        if not pos64 and pos.dtype is not torch.int32:
             raise TypeError(f"positions must be int32 or int64, got {pos.dtype}")
-        pos64, pp = int(pos.dtype == torch.int64), pos.data_ptr()
-    ap = _small(axis, dev, torch.uint8, (R // 2,), "axis")
+        if pos.get_device() != index:
+            raise ValueError("all tensors must be on the same CUDA device")
+        pp = pos.data_ptr()
+    ap = 0 if axis is None else _small(axis, torch.uint8, index, (half,), "axis")
     Hk, ka, ko = 0, _NO_ROWS, _NO_ROWS
     if k is not None:
         Hk = _four(k, "k")[1]
-        ka = _rows(k, q, (B, Hk, n, D), "k")
+        ka = _rows(k, dtype, index, (B, Hk, n, D), "k")
         if k_out is None:
             k_out = torch.empty_like(k)
-        ko = _rows(k_out, q, k.shape, "k_out")
+        ko = _rows(k_out, dtype, index, k.shape, "k_out")
     if q_out is None:
         q_out = torch.empty_like(q)
-    qo = _rows(q_out, q, shape, "q_out")
-    _call(dev, lib.rehyat_rotary, _ROTARY.pack(
-        B, n, H, Hk, D, R, interleaved, inverse, axes, pos64, add, code, pa, pb, pn, start, fp, ap,
-        pp, *qa, *ka, *qo, *ko, scale))
+    qo = _rows(q_out, dtype, index, shape, "q_out")
+    _call(index, lib.rehyat_rotary, _ROTARY.pack(
+        B, n, H, Hk, D, 2 * half, interleaved, inverse, axes, pos64, add, code, pa, pb, pn, start,
+        fp, ap, pp, *qa, *ka, *qo, *ko, scale))
     return q_out if k is None else (q_out, k_out)
 
 
@@ -867,23 +876,25 @@ def decay_forward(q, k, v, log_decay, *, scale: float = 1.0, lengths: torch.Tens
     `decay_step` or the next call goes on from; a tensor: written there (it may be `state`)."""
     lib = _lib or load()
     B, H, Hk, N, D = _decay_sizes(q, k)
-    dev, code = q.device, _dtype_code(q)
+    dtype, code, index = _typed(q)
     shape, kv, square = q.shape, (B, Hk, N, D), (B, H, D, D)
-    qa, ka, va = _rows(q, q, shape, "q"), _rows(k, q, kv, "k"), _rows(v, q, kv, "v")
-    gp = _small(log_decay, _cuda(dev), torch.float32, (H,), "log_decay")
-    lp = _small(lengths, dev, torch.int32, (B,), "lengths")
-    sp = _small(state, dev, torch.float32, square, "state")
+    qa = _rows(q, dtype, index, shape, "q")
+    ka, va = _rows(k, dtype, index, kv, "k"), _rows(v, dtype, index, kv, "v")
+    gp = _small(log_decay, torch.float32, index, (H,), "log_decay")
+    lp = 0 if lengths is None else _small(lengths, torch.int32, index, (B,), "lengths")
+    sp = 0 if state is None else _small(state, torch.float32, index, square, "state")
     if out is None:
         out = torch.empty_like(q)
-    oa = _rows(out, q, shape, "out")
-    last = None
+    oa = _rows(out, dtype, index, shape, "out")
+    last, fp = None, 0
     if isinstance(final_state, torch.Tensor):
         last = final_state
+        fp = _small(last, torch.float32, index, square, "final_state")
     elif final_state:
-        last = torch.empty(square, dtype=torch.float32, device=dev)
-    fp = _small(last, dev, torch.float32, square, "final_state")
-    ws = _scratch(decay_workspace_size(B, H, Hk, N, D), dev, workspace)
-    _call(dev, lib.rehyat_decay_forward, _DECAY_FORWARD.pack(
+        last = torch.empty(square, dtype=torch.float32, device=q.device)
+        fp = last.data_ptr()
+    ws = _scratch(decay_workspace_size(B, H, Hk, N, D), q.device, workspace)
+    _call(index, lib.rehyat_decay_forward, _DECAY_FORWARD.pack(
         B, H, Hk, N, D, code, *qa, *ka, *va, *oa, gp, lp, sp, fp, ws.data_ptr(), ws.numel(), scale))
     return out if last is None else (out, last)
 
@@ -898,22 +909,24 @@ def decay_backward(q, k, v, log_decay, dout, *, scale: float = 1.0,
     [B,H,D,D] fp32 or None (zero)."""
     lib = _lib or load()
     B, H, Hk, N, D = _decay_sizes(q, k)
-    dev, code = q.device, _dtype_code(q)
+    dtype, code, index = _typed(q)
     shape, kv, square = q.shape, (B, Hk, N, D), (B, H, D, D)
-    qa, ka, va = _rows(q, q, shape, "q"), _rows(k, q, kv, "k"), _rows(v, q, kv, "v")
-    doa = _rows(dout, q, shape, "dout")
-    gp = _small(log_decay, _cuda(dev), torch.float32, (H,), "log_decay")
-    lp = _small(lengths, dev, torch.int32, (B,), "lengths")
-    sp = _small(state, dev, torch.float32, square, "state")
-    fp = _small(dfinal, dev, torch.float32, square, "dfinal")
+    qa = _rows(q, dtype, index, shape, "q")
+    ka, va = _rows(k, dtype, index, kv, "k"), _rows(v, dtype, index, kv, "v")
+    doa = _rows(dout, dtype, index, shape, "dout")
+    gp = _small(log_decay, torch.float32, index, (H,), "log_decay")
+    lp = 0 if lengths is None else _small(lengths, torch.int32, index, (B,), "lengths")
+    sp = 0 if state is None else _small(state, torch.float32, index, square, "state")
+    fp = 0 if dfinal is None else _small(dfinal, torch.float32, index, square, "dfinal")
     g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v)}
     if state is not None:
-        g["dstate"] = torch.empty(square, dtype=torch.float32, device=dev)
-    ws = _scratch(decay_workspace_size(B, H, Hk, N, D, True), dev, workspace)
-    _call(dev, lib.rehyat_decay_backward, _DECAY_BACKWARD.pack(
-        B, H, Hk, N, D, code, *qa, *ka, *va, *doa, *_rows(g["dq"], q, shape, "dq"),
-        *_rows(g["dk"], q, kv, "dk"), *_rows(g["dv"], q, kv, "dv"), gp, lp, sp, fp,
-        g["dstate"].data_ptr() if state is not None else 0, ws.data_ptr(), ws.numel(), scale))
+        g["dstate"] = torch.empty(square, dtype=torch.float32, device=q.device)
+    ws = _scratch(decay_workspace_size(B, H, Hk, N, D, True), q.device, workspace)
+    _call(index, lib.rehyat_decay_backward, _DECAY_BACKWARD.pack(
+        B, H, Hk, N, D, code, *qa, *ka, *va, *doa, *_rows(g["dq"], dtype, index, shape, "dq"),
+        *_rows(g["dk"], dtype, index, kv, "dk"), *_rows(g["dv"], dtype, index, kv, "dv"), gp, lp,
+        sp, fp, g["dstate"].data_ptr() if state is not None else 0, ws.data_ptr(), ws.numel(),
+        scale))
     return g
 
 
@@ -928,15 +941,17 @@ def decay_step(q, k, v, log_decay, state, *, scale: float = 1.0,
     B, H, Hk, N, D = _decay_sizes(q, k)
     if N != 1:
         raise ValueError(f"a step takes one token of each sequence, got {N}")
-    dev, code = q.device, _dtype_code(q)
+    dtype, code, index = _typed(q)
     shape, kv = q.shape, (B, Hk, 1, D)
     pool = state.shape[0] if slots is not None and state.dim() == 4 else B
-    qa, ka, va = _rows(q, q, shape, "q"), _rows(k, q, kv, "k"), _rows(v, q, kv, "v")
-    gp = _small(log_decay, _cuda(dev), torch.float32, (H,), "log_decay")
-    sp = _small(state, dev, torch.float32, (pool, H, D, D), "state")
-    lp = _small(slots, dev, torch.int32, (B,), "slots")
+    qa = _rows(q, dtype, index, shape, "q")
+    ka, va = _rows(k, dtype, index, kv, "k"), _rows(v, dtype, index, kv, "v")
+    gp = _small(log_decay, torch.float32, index, (H,), "log_decay")
+    sp = _small(state, torch.float32, index, (pool, H, D, D), "state")
+    lp = 0 if slots is None else _small(slots, torch.int32, index, (B,), "slots")
     if out is None:
         out = torch.empty_like(q)
-    _call(dev, lib.rehyat_decay_step, _DECAY_STEP.pack(
-        B, H, Hk, D, pool, code, *qa, *ka, *va, *_rows(out, q, shape, "out"), gp, sp, lp, scale))
+    _call(index, lib.rehyat_decay_step, _DECAY_STEP.pack(
+        B, H, Hk, D, pool, code, *qa, *ka, *va, *_rows(out, dtype, index, shape, "out"), gp, sp, lp,
+        scale))
     return out
