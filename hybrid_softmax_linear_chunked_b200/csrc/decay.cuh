@@ -18,8 +18,8 @@
 // so that the kernels' threads, one row each, read and write neighbouring float4s (by rows, a state
 // took a row-pass CTA 3.8 us to read and a states CTA 2.9 us to write).
 //
-// A sequence is cut into segments of whole chunks.  Three launches: the sum of every
-// segment's own rows (decay_states), its exclusive prefix in time order (decay_scan), and the rows
+// Sequences are cut into segments of whole chunks (Cut).  Three launches: the sum of every segment's
+// own rows (decay_states), its exclusive prefix in time order (decay_scan), and the rows
 // of every segment, chunk after chunk with the state carried along (decay_rows).  Every exponent
 // above is >= 0, so no power grows for L <= 1 and none is divided by; L = 0 (log_decay = -inf)
 // leaves each row its own term.
@@ -47,19 +47,26 @@ struct Rows {
   int group;
 };
 
+// How sequences are cut: into segments of `chunks` chunks of `chunk` rows, segment s of sequence b in
+// slot b * per_seq + s.  With `search` (ragged batches) the segments are instead the shortest that
+// fit all sequences' valid rows into the slots, one sequence's behind the other's.  One CTA for each
+// slot and head.
+struct Cut {
+  int chunk, chunks, per_seq, slots, search;
+};
+
 struct Pass {
   Rows a, b, c;
   void* out;                 // row type, or fp32 where the group sum follows
   long long ob, oh, on;      // its strides
   const float* log_decay;    // [H]
   const int* lengths;        // [B] or null: rows at and past a sequence's length are padding
-  const float* prefix;       // [B*H][nseg] states before each segment in time, or null (zero)
-  float* delta;              // [B*H][nseg] states: each segment's own sum
+  float* states;             // [slots][H] each segment's own sum, then the state before it
   int B, H, N, D;
-  int nseg, seg_rows;
+  Cut cut;
   int reverse, e;
-  int transposed;            // the pass's state is the transpose of `prefix`
-  int seg_skip;              // states: the segment whose sum nothing reads, or -1
+  int carried;               // rows: segments have a state before them (else zero)
+  int transposed;            // rows: the pass's state is the transpose of `states`
   int exact;                 // states: the last state is given out (bf16: two-part products)
   int out_f32;               // rows: fp32 output for the group sum
   float sp, si, sd;
@@ -75,6 +82,108 @@ __device__ __forceinline__ float log2_decay(const float* g, int h) {
 }
 __device__ __forceinline__ int length_of(const int* lengths, int b, int N) {
   return lengths ? min(max(lengths[b], 0), N) : N;
+}
+
+__device__ __forceinline__ int chunks_of(const int* lengths, int b, int N, int chunk) {
+  return (length_of(lengths, b, N) + chunk - 1) / chunk;
+}
+// A ragged batch's cut, by one warp (all lanes; at most kMaxSearch sequences): the fewest chunks a
+// segment with which the sequences' segments fit into the slots, by bisection between the mean and
+// the longest.  A lane holds every 32nd sequence.  (By the whole block, with a barrier for each sum,
+// it took 5 us of every launch.)
+constexpr int kMaxSearch = 256;
+struct Search {
+  int n[kMaxSearch / 32];  // chunks of sequences lane, lane + 32, ...
+  int per;
+
+  __device__ __forceinline__ Search(const Cut& cut, const int* lengths, int B, int N) {
+    const int lane = threadIdx.x & 31;
+    unsigned total = 0;
+#pragma unroll
+    for (int k = 0; k < kMaxSearch / 32; ++k) {
+      const int b = lane + 32 * k;
+      n[k] = b < B ? chunks_of(lengths, b, N, cut.chunk) : 0;
+      total += n[k];
+    }
+    total = __reduce_add_sync(0xffffffffu, total);
+    int lo = max((int)((total + cut.slots - 1) / cut.slots), 1);
+    int hi = max(cut.chunks * cut.per_seq, lo);
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      unsigned used = 0;
+#pragma unroll
+      for (int k = 0; k < kMaxSearch / 32; ++k)
+        if (32 * k < B) used += (unsigned)(n[k] + mid - 1) / (unsigned)mid;
+      if ((int)__reduce_add_sync(0xffffffffu, used) <= cut.slots)
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    per = lo;
+  }
+  // Slots of the sequences before b, and in all (b >= the batch).
+  __device__ __forceinline__ int slots_before(int b) const {
+    unsigned used = 0;
+#pragma unroll
+    for (int k = 0; k < kMaxSearch / 32; ++k)
+      if ((int)(threadIdx.x & 31) + 32 * k < b) used += (unsigned)(n[k] + per - 1) / (unsigned)per;
+    return (int)__reduce_add_sync(0xffffffffu, used);
+  }
+};
+
+// Segment of this CTA (head blockIdx.x, slot blockIdx.y): valid rows [begin, end) of sequence b; none
+// if begin >= end.  All threads of the block call it.
+struct Segment {
+  int b, h, begin, end;
+  bool last;  // in time
+};
+__device__ __forceinline__ Segment find_segment(const Pass& p) {
+  __shared__ int found[3];
+  const int slot = blockIdx.y;
+  int b, s, per = p.cut.chunks;
+  if (!p.cut.search) {
+    b = slot / p.cut.per_seq;
+    s = slot - b * p.cut.per_seq;
+  } else {
+    if (threadIdx.x < 32) {
+      const Search f(p.cut, p.lengths, p.B, p.N);
+      if (threadIdx.x == 0) found[0] = -1;
+      __syncwarp();
+      int base = 0;  // slots of the sequences before: 32 sequences a turn
+#pragma unroll
+      for (int k = 0; k < kMaxSearch / 32; ++k) {
+        const int n = (f.n[k] + f.per - 1) / f.per;
+        int end = n;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, end, m);
+          if ((int)threadIdx.x >= m) end += y;
+        }
+        end += base;
+        if (end - n <= slot && slot < end) {
+          found[0] = threadIdx.x + 32 * k;
+          found[1] = slot - (end - n);
+        }
+        base = __shfl_sync(0xffffffffu, end, 31);
+        if (base > slot) break;
+      }
+      if (threadIdx.x == 0) found[2] = f.per;
+    }
+    __syncthreads();
+    b = found[0];
+    s = found[1];
+    per = found[2];
+    if (b < 0) return Segment{0, (int)blockIdx.x, 0, 0, false};
+  }
+  const int len = length_of(p.lengths, b, p.N), rows = per * p.cut.chunk;
+  Segment g{b, (int)blockIdx.x, s * rows, 0, false};
+  g.end = min(len, g.begin + rows);
+  g.last = p.reverse ? s == 0 : g.end == len;
+  return g;
+}
+// This CTA's state in the workspace.
+__device__ __forceinline__ float* state_of(const Pass& p) {
+  return p.states + ((size_t)blockIdx.y * p.H + blockIdx.x) * p.D * p.D;
 }
 
 template <typename T>
@@ -161,24 +270,23 @@ __device__ __forceinline__ void outer_add(uint64_t (&acc)[kDp / 16][kDp / 32], c
   }
 }
 
-// Each segment's own sum: delta = sd * sum_j L^(n - t_j - e) b_j c_j^T over its n valid rows.
-// grid (nseg, B*H, n), block 256.
+// Each segment's own sum: sd * sum_j L^(n - t_j - e) b_j c_j^T over its n valid rows.
+// grid (H, slots, passes), block 256.
 template <int kDp>
 __global__ void __launch_bounds__(kThreads, kDp <= 64 ? 2 : 1)
     decay_states_kernel(const __grid_constant__ Passes all) {
   extern __shared__ __align__(16) float smf[];
   sm100::grid_dep_signal();
   const Pass& p = all.p[blockIdx.z];
-  const int seg = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh - b * p.H;
-  if (seg == p.seg_skip) return;
+  const Segment seg = find_segment(p);
+  const int b = seg.b, h = seg.h, r_begin = seg.begin, r_end = seg.end;
+  if (r_begin >= r_end || (seg.last && !p.exact)) return;  // nothing reads its sum
   constexpr int n = kDp / 32, ld = kDp + 4;
   const int tid = threadIdx.x;
   float* sb = smf;
   float* sc = sb + kC * ld;
   float* sw = sc + kC * ld;
   const float g2 = log2_decay(p.log_decay, h);
-  const int r_begin = seg * p.seg_rows;
-  const int r_end = min(r_begin + p.seg_rows, length_of(p.lengths, b, p.N));
   uint64_t acc[2 * n][n];
 #pragma unroll
   for (int i = 0; i < 2 * n; ++i)
@@ -195,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, kDp <= 64 ? 2 : 1)
     __syncthreads();
     outer_add<kDp>(acc, sb, sc, sw, min(kC, r_end - r0));
   }
-  float* dst = p.delta + ((size_t)bh * p.nseg + seg) * p.D * p.D;
+  float* dst = state_of(p);
   const int i0 = (tid / 16) * 2, j0 = (tid % 16) * 2;
 #pragma unroll
   for (int i = 0; i < 2 * n; ++i)
@@ -211,38 +319,51 @@ __global__ void __launch_bounds__(kThreads, kDp <= 64 ? 2 : 1)
 // after the last: state_{s+1} = L^(rows of s) state_s + delta_s.  S0 and last are stored by rows and
 // may be the same buffer (each element is read before it is written, by one thread).
 struct Scan {
-  float* delta;
+  float* states;
   const float* S0;
   float* last;
-  int reverse, need_prefix;
+  int reverse;
 };
 struct Scans {
   Scan s[2];
   const float* log_decay;
   const int* lengths;
-  int H, N, D, nseg, seg_rows;
+  int B, H, N, D;
+  Cut cut;
 };
 // grid (ceil(D*D/4 / 256), B*H, scans), block 256.
-__global__ void __launch_bounds__(256) decay_scan_kernel(const __grid_constant__ Scans a) {
+__global__ void __launch_bounds__(256, 4) decay_scan_kernel(const __grid_constant__ Scans a) {
   sm100::grid_dep_signal();
-  float* delta = a.s[blockIdx.z].delta;
   const float* S0 = a.s[blockIdx.z].S0;
   float* last = a.s[blockIdx.z].last;
-  const int reverse = a.s[blockIdx.z].reverse, need_prefix = a.s[blockIdx.z].need_prefix;
-  const int H = a.H, N = a.N, D = a.D, nseg = a.nseg, seg_rows = a.seg_rows;
-  const float* log_decay = a.log_decay;
-  const int* lengths = a.lengths;
+  const int reverse = a.s[blockIdx.z].reverse, H = a.H, D = a.D;
   const int bh = blockIdx.y, b = bh / H, h = bh - b * H;
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  const int n4 = D * D / 4;
+  const int n4 = D * D / 4, i = blockIdx.x * 256 + threadIdx.x;
+  const int at = (i % D) * (D / 4) + i / D;  // of a state stored by rows
+  const float g2 = log2_decay(a.log_decay, h);
+  const int n = length_of(a.lengths, b, a.N);
+  int per = a.cut.chunks, slot = b * a.cut.per_seq;
+  if (a.cut.search) {
+    __shared__ int found[2];
+    if (threadIdx.x < 32) {
+      const Search f(a.cut, a.lengths, a.B, a.N);
+      const int before = f.slots_before(b);
+      if (threadIdx.x == 0) {
+        found[0] = f.per;
+        found[1] = before;
+      }
+    }
+    __syncthreads();
+    per = found[0];
+    slot = found[1];
+  }
+  const int seg_rows = per * a.cut.chunk, nseg = (n + seg_rows - 1) / seg_rows;
   sm100::grid_dep_wait();
   if (i >= n4) return;
-  const float g2 = log2_decay(log_decay, h);
-  const int n = length_of(lengths, b, N);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int at = (i % D) * (D / 4) + i / D;  // of a state stored by rows
   if (S0) acc = reinterpret_cast<const float4*>(S0)[(size_t)bh * n4 + at];
-  float4* d = reinterpret_cast<float4*>(delta) + (size_t)bh * nseg * n4 + i;
+  float4* d = reinterpret_cast<float4*>(a.s[blockIdx.z].states) + ((size_t)slot * H + h) * n4 + i;
+  const size_t stride = (size_t)H * n4;
   const int steps = last ? nseg : nseg - 1;  // the last segment's sum is only in the last state
   // eight segments' sums are loaded before any is written over, so their latencies overlap
   for (int t0 = 0; t0 < nseg; t0 += 8) {
@@ -251,29 +372,54 @@ __global__ void __launch_bounds__(256) decay_scan_kernel(const __grid_constant__
     for (int u = 0; u < 8; ++u) {
       const int t = t0 + u, s = reverse ? nseg - 1 - t : t;
       add[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (t < steps && n > s * seg_rows) add[u] = d[(size_t)s * n4];
+      if (t < steps) add[u] = d[s * stride];
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int t = t0 + u, s = reverse ? nseg - 1 - t : t;
       if (t >= nseg) break;
-      const int rows = min(max(n - s * seg_rows, 0), seg_rows);
-      if (need_prefix) d[(size_t)s * n4] = acc;
-      if (t < steps && rows > 0) acc = fma4(exp2f(g2 * (float)rows), acc, add[u]);
+      d[s * stride] = acc;
+      if (t < steps) acc = fma4(exp2f(g2 * (float)min(n - s * seg_rows, seg_rows)), acc, add[u]);
     }
   }
   if (last) reinterpret_cast<float4*>(last)[(size_t)bh * n4 + at] = acc;
 }
 
+// Zeros in the output rows of whole chunks of padding, by `n` threads of each CTA, this one the t-th.
+// A pair's padding is dealt out in sixteen parts, one CTA after the other: left to one CTA, the
+// padding of an empty sequence took as long as the rows of the others.  kBytes: of an element.
+template <int kBytes>
+__device__ __forceinline__ void zero_padding(const Pass& p, int t, int n) {
+  if (!p.lengths) return;
+  constexpr int kParts = 16;
+  const int vec = p.D * kBytes / 16;
+  for (int u = blockIdx.y * gridDim.x + blockIdx.x; u < p.B * p.H * kParts;
+       u += gridDim.x * gridDim.y) {
+    const int bh = u / kParts, part = u % kParts, b = bh / p.H, h = bh - b * p.H;
+    const int z0 = chunks_of(p.lengths, b, p.N, p.cut.chunk) * p.cut.chunk;
+    if (z0 >= p.N) continue;
+    const int rows = (p.N - z0 + kParts - 1) / kParts, r0 = z0 + part * rows;
+    uint8_t* out = static_cast<uint8_t*>(p.out) + (b * p.ob + h * p.oh + r0 * p.on) * kBytes;
+    const int items = max(0, min(rows, p.N - r0)) * vec;
+    for (int i = t; i < items; i += n) {
+      const int r = i / vec;
+      *reinterpret_cast<uint4*>(out + r * p.on * kBytes + (i - r * vec) * 16) =
+          make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
 // The rows of one segment: chunks of kC in time order, the state carried in shared memory.
 // Bound by the fp32 pipes: kC D (kC + kC / 2 + 2 D) multiply-adds a chunk.
-// grid (nseg, B*H, n), block 256.
+// grid (H, slots, passes), block 256.
 template <int kDp>
 __global__ void __launch_bounds__(kThreads, kDp <= 64 ? 2 : 1)
     decay_rows_kernel(const __grid_constant__ Passes all) {
   extern __shared__ __align__(16) float smf[];
   const Pass& p = all.p[blockIdx.z];
-  const int seg = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh - b * p.H;
+  const Segment seg = find_segment(p);
+  const int b = seg.b, h = seg.h, r_begin = seg.begin, r_end = seg.end;
+  zero_padding<4>(p, threadIdx.x, kThreads);
   constexpr int n = kDp / 32, ld = kDp + 4, ldp = kC + 4;
   float* sa = smf;
   float* sb = sa + kC * ld;
@@ -284,18 +430,16 @@ __global__ void __launch_bounds__(kThreads, kDp <= 64 ? 2 : 1)
   float* sw = spow + kC;        // weights of b's rows
   const int tid = threadIdx.x, warp = tid >> 5;
   const float g2 = log2_decay(p.log_decay, h);
-  const int len = length_of(p.lengths, b, p.N);
-  const int r_begin = seg * p.seg_rows, r_stop = min(r_begin + p.seg_rows, p.N);
-  const int r_end = min(r_stop, len);
   float* out = static_cast<float*>(p.out) + b * p.ob + h * p.oh;
   if (tid < kC) spow[tid] = p.sp * exp2f(g2 * (float)tid);
 
-  sm100::grid_dep_wait();  // the prefix comes from the launch before
+  sm100::grid_dep_wait();  // the states come from the launch before
+  if (r_begin >= r_end) return;
   for (int i = tid; i < kDp * (kDp / 4); i += kThreads) {
     const int r = i % kDp, c = (i / kDp) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (p.prefix && r < p.D && c < p.D) {
-      const float* src = p.prefix + ((size_t)bh * p.nseg + seg) * p.D * p.D;
+    if (p.carried && r < p.D && c < p.D) {
+      const float* src = state_of(p);
       if (p.transposed) {
         const float* col = src + (r >> 2) * 4 * p.D + c * 4 + (r & 3);
         x = make_float4(col[0], col[4], col[8], col[12]);
@@ -305,20 +449,12 @@ __global__ void __launch_bounds__(kThreads, kDp <= 64 ? 2 : 1)
     }
     *reinterpret_cast<float4*>(ss + r * ld + c) = x;
   }
-  const int nc = (r_stop - r_begin + kC - 1) / kC;
+  const int nc = (r_end - r_begin + kC - 1) / kC;
   const int i4 = (tid / 16) * 4, j2 = (tid % 16) * 2;  // rows i4 .. i4 + 3, column pairs from j2
   for (int ci = 0; ci < nc; ++ci) {
     const int r0 = r_begin + (p.reverse ? nc - 1 - ci : ci) * kC;
-    const int rows = min(max(r_end - r0, 0), kC);  // valid rows
+    const int rows = min(r_end - r0, kC);  // valid rows
     __syncthreads();
-    if (rows == 0) {  // nothing but padding: zeros, the state stays
-      for (int i = tid; i < kC * (kDp / 4); i += kThreads) {
-        const int r = i / (kDp / 4), c = (i % (kDp / 4)) * 4;
-        if (r0 + r < r_stop && c < p.D)
-          store4(out + (long long)(r0 + r) * p.on + c, make_float4(0.f, 0.f, 0.f, 0.f));
-      }
-      continue;
-    }
     load_rows<kDp>(sa, p.a, b, h, r0, r_end, p.D);
     load_rows<kDp>(sb, p.b, b, h, r0, r_end, p.D);
     load_rows<kDp>(sc, p.c, b, h, r0, r_end, p.D);
@@ -391,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, kDp <= 64 ? 2 : 1)
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int r = i4 + u;
-        if (r0 + r >= r_stop) continue;
+        if (r0 + r >= p.N) continue;
         float* dst = out + (long long)(r0 + r) * p.on;
 #pragma unroll
         for (int v = 0; v < n; ++v)

@@ -75,7 +75,7 @@ __device__ __forceinline__ uint4 mul8(uint4 x, __nv_bfloat162 w) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// States: delta = sd * sum_j L^(n - t_j - e) b_j c_j^T over a segment.
+// States: sd * sum_j L^(n - t_j - e) b_j c_j^T over a segment.
 // ---------------------------------------------------------------------------------------------
 constexpr int kStStages = 3;
 constexpr int kStHalf = 256;                   // warps 0-7 weigh rows 0-63 of a chunk, 8-15 the rest
@@ -83,7 +83,7 @@ constexpr int kStIn = 16, kStMma = 17;         // copies, products
 constexpr int kStThreads = 2 * kStHalf + 64;
 constexpr uint32_t kStOffLo = kStStages * 2 * kTile;
 constexpr uint32_t kStSmem = kStOffLo + kTile + 1024;
-static_assert(kStSmem + 256 <= 232448, "shared memory over the limit");
+static_assert(kStSmem + 1024 <= 232448, "shared memory over the limit");
 
 // Every weight is taken to the segment's end, so chunks add up without rescaling, in any order.
 // They run in the order opposite to the row pass that follows: what was read last (and may still be
@@ -98,17 +98,14 @@ static_assert(kStSmem + 256 <= 232448, "shared memory over the limit");
 constexpr int kFlush = 8, kLate = 2;
 template <bool kTwo>
 __device__ __forceinline__ void states_of_segment(const CUtensorMap& tmB, const CUtensorMap& tmC,
-                                                  const Pass& p, int seg) {
+                                                  const Pass& p, const Segment& seg) {
   enum {
     kFull = 0, kEmpty = kFull + kStStages, kReady = kEmpty + kStStages,  // kReady: [half][stage]
     kLoFree = kReady + 2 * kStStages, kSummed = kLoFree + 2, kDone, kNum
   };
-  const int bh = blockIdx.y, b = bh / p.H, h = bh - b * p.H;
-  if (seg == p.seg_skip) return;
-  const int r_begin = seg * p.seg_rows;
-  const int r_end = min(r_begin + p.seg_rows, length_of(p.lengths, b, p.N));
+  const int b = seg.b, h = seg.h, r_begin = seg.begin, r_end = seg.end;
   const int nc = (r_end - r_begin + kRows - 1) / kRows;
-  if (nc <= 0) return;  // the scan does not read the sum of no rows
+  if (nc <= 0 || (seg.last && !p.exact)) return;  // nothing reads its sum
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
@@ -243,7 +240,7 @@ __device__ __forceinline__ void states_of_segment(const CUtensorMap& tmB, const 
       const int group = (nc - 1) / kFlush;
       if (group > 0 && (nc - 1) % kFlush < kLate) flush(group - 1);
       flush(group);
-      float* dst = p.delta + ((size_t)bh * p.nseg + seg) * p.D * p.D + rs * 4;
+      float* dst = state_of(p) + rs * 4;
       if (rs < p.D) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -268,11 +265,12 @@ struct StatesArgs {
   Pass p[2];
   CUtensorMap b[2], c[2];
 };
-// grid (nseg, B*H, n), block 576.
+// grid (H, slots, passes), block 576.
 __global__ void __launch_bounds__(kStThreads, 1)
     decay_states_bf16_kernel(const __grid_constant__ StatesArgs a) {
   grid_dep_signal();
-  const int w = blockIdx.z, seg = blockIdx.x;
+  const int w = blockIdx.z;
+  const Segment seg = find_segment(a.p[w]);
   if (a.p[w].exact)
     states_of_segment<true>(a.b[w], a.c[w], a.p[w], seg);
   else
@@ -294,6 +292,8 @@ static_assert(kRwSmem + 2048 <= 232448 + 512, "shared memory over the limit");
 // TMEM columns: scores a b^T (P over them), P c, a S, the chunk's own b^T c
 constexpr uint32_t kColP = 0, kColIn = 128, kColSt = 256, kColAdd = 384;
 
+// No barrier completes a phase ahead of a thread that has yet to wait for the one before: each is
+// either armed by that thread's own earlier step or, like kStaged, has one for each stage.
 // A chunk i, chunk after chunk in time order:
 //   scores = a b^T -> P = sp L^|i-j| scores on the past, bf16, into TMEM     (warps 0-7)
 //   b weighted in place (after the scores have read it)                       (warps 8-15)
@@ -304,28 +304,16 @@ constexpr uint32_t kColP = 0, kColIn = 128, kColSt = 256, kColAdd = 384;
 template <bool kReverse, bool kOutF32>
 __device__ __forceinline__ void rows_of_segment(const CUtensorMap& tmA, const CUtensorMap& tmB,
                                                 const CUtensorMap& tmC, const CUtensorMap& tmOut,
-                                                const Pass& p, int seg) {
+                                                const Pass& p, const Segment& seg) {
   enum {
     kAFull = 0, kBFull = 2, kCFull = 4, kAEmpty = 6, kBEmpty = 8, kCEmpty = 10, kScores = 12,
-    kPReady, kBReady, kOFull, kAddFull, kStaged, kDone, kNum
+    kPReady, kBReady, kOFull, kAddFull, kStaged, kDone = kStaged + 2, kNum
   };
-  const int bh = blockIdx.y, b = bh / p.H, h = bh - b * p.H;
-  const int r_begin = seg * p.seg_rows, r_stop = min(r_begin + p.seg_rows, p.N);
-  const int r_end = min(r_stop, length_of(p.lengths, b, p.N));
-  const int nc = max(0, (r_end - r_begin + kRows - 1) / kRows);  // chunks that hold valid rows
+  const int b = seg.b, h = seg.h, r_begin = seg.begin, r_end = seg.end;
+  const int nc = (r_end - r_begin + kRows - 1) / kRows;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-
-  // rows of whole chunks of padding
-  {
-    const int z0 = r_begin + nc * kRows, vec = p.D * (kOutF32 ? 4 : 2) / 16;
-    uint8_t* out = static_cast<uint8_t*>(p.out);
-    for (long long i = tid; i < (long long)max(0, r_stop - z0) * vec; i += kRwThreads) {
-      const int r = z0 + (int)(i / vec), v = (int)(i % vec);
-      const long long el = b * p.ob + h * p.oh + r * p.on;
-      *reinterpret_cast<uint4*>(out + el * (kOutF32 ? 4 : 2) + v * 16) = make_uint4(0, 0, 0, 0);
-    }
-  }
-  if (nc == 0) {
+  if (nc <= 0) {
+    zero_padding<kOutF32 ? 4 : 2>(p, tid, kRwThreads);
     grid_dep_wait();
     return;
   }
@@ -348,7 +336,7 @@ __device__ __forceinline__ void rows_of_segment(const CUtensorMap& tmA, const CU
   }
   if (tid == 0) {
     for (int i = 0; i < kNum; ++i) {
-      const bool many = i == kPReady || i == kBReady || i == kStaged;
+      const bool many = i == kPReady || i == kBReady || i == kStaged || i == kStaged + 1;
       mbar_init(&bars[i], many ? 256 : 1);
     }
     abort_sh = 0;
@@ -358,7 +346,7 @@ __device__ __forceinline__ void rows_of_segment(const CUtensorMap& tmA, const CU
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_sh;
-  const bool carried = p.prefix != nullptr;  // chunk 0 has a state to read
+  const bool carried = p.carried;  // chunk 0 has a state to read
   auto wait = [&](int bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(&bars[bar], parity, abort_flag));
   };
@@ -464,7 +452,7 @@ __device__ __forceinline__ void rows_of_segment(const CUtensorMap& tmA, const CU
   } else if (warp == kRwOut) {  // ---- copies out; c's tile is free once the output has left it ----
     bool ok = true;
     for (int i = 0; i < nc && ok; ++i) {
-      ok = wait(kStaged, i & 1);
+      ok = wait(kStaged + (i & 1), (i >> 1) & 1);
       if (!ok) break;
       if (lane == 0) {
         if (!kOutF32) {
@@ -583,7 +571,7 @@ __device__ __forceinline__ void rows_of_segment(const CUtensorMap& tmA, const CU
 #pragma unroll
           for (int j = 0; j < 16; ++j) o[j] = 0ull;
         if (kOutF32) {
-          if (row0 + r < r_stop)
+          if (row0 + r < p.N)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               if (c0 + j * 4 < p.D) {
@@ -602,7 +590,7 @@ __device__ __forceinline__ void rows_of_segment(const CUtensorMap& tmA, const CU
       }
       tc_fence_before();
       fence_async_smem();
-      mbar_arrive(&bars[kStaged]);
+      mbar_arrive(&bars[kStaged + (i & 1)]);
     }
   } else {  // ---- weights and the state: row r of b's tile, and row r of S = TMEM lane ----
     const int r = tid & 127, c0 = ((warp - 8) >> 2) * 64;
@@ -618,9 +606,10 @@ __device__ __forceinline__ void rows_of_segment(const CUtensorMap& tmA, const CU
         *reinterpret_cast<uint4*>(sS + sw128_offset(r, c0 + j * 8, kRows)) = make_uint4(
             f2_bf16(S[j * 4]), f2_bf16(S[j * 4 + 1]), f2_bf16(S[j * 4 + 2]), f2_bf16(S[j * 4 + 3]));
     };
-    grid_dep_wait();  // the prefix comes from the launch before
+    zero_padding<kOutF32 ? 4 : 2>(p, tid - 256, 256);  // nothing else to do yet
+    grid_dep_wait();  // the states come from the launch before
     if (carried && r < p.D) {
-      const float* src = p.prefix + ((size_t)bh * p.nseg + seg) * p.D * p.D;
+      const float* src = state_of(p);
       // loads in batches, before any is used
       if (p.transposed) {
         const float* col = src + (r >> 2) * 4 * p.D + c0 * 4 + (r & 3);
@@ -715,11 +704,12 @@ struct RowsArgs {
   Pass p[3];
   CUtensorMap a[3], b[3], c[3], out[3];
 };
-// grid (nseg, B*H, n), block 608.
+// grid (H, slots, passes), block 608.
 __global__ void __launch_bounds__(kRwThreads, 1)
     decay_rows_bf16_kernel(const __grid_constant__ RowsArgs a) {
-  const int w = blockIdx.z, seg = blockIdx.x;
+  const int w = blockIdx.z;
   const Pass& p = a.p[w];
+  const Segment seg = find_segment(p);
   if (!p.reverse)
     rows_of_segment<false, false>(a.a[w], a.b[w], a.c[w], a.out[w], p, seg);
   else if (!p.out_f32)

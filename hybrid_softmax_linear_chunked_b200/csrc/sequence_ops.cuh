@@ -61,43 +61,51 @@ Rows rows_of(const rehyat_rows& s, int group) {
   return Rows{s.p, s.batch, s.head, s.row, group};
 }
 
-// Segments of a sequence: one CTA each, so their number trades whole waves of the 148 SMs against
-// each CTA's start, about one chunk of the bf16 kernels (128 rows) and a quarter of one of the fp32
-// kernels (64 rows).  A launch of three passes takes the same cut: each pass fills the waves by
-// itself (cut for all three at once, in one wave of 64-chunk segments, the 480x832 5 s gradients took
-// 380 us instead of 320).
-struct Segments {
-  int n, rows;
-};
-Segments decay_segments(int BH, int N, rehyat_dtype dt) {
-  const int chunk = dt == REHYAT_BF16 ? rehyat::decay::tc::kRows : rehyat::decay::kC;
-  const int start = dt == REHYAT_BF16 ? 4 : 1;  // in quarters of a chunk
-  const int chunks = N > 0 ? (N + chunk - 1) / chunk : 1;
-  Segments best{1, chunks * chunk};
-  long long best_cost = -1;
+// The cut of sequences into segments: one CTA for each and each head, so their number trades whole
+// waves of the 148 SMs against each CTA's start, about one chunk of the bf16 kernels (128 rows) and a
+// quarter of one of the fp32 kernels (64 rows).  A launch of three passes takes the same cut: each
+// pass fills the waves by itself (cut for all three at once, in one wave of 64-chunk segments, the
+// 480x832 5 s gradients took 380 us instead of 320).  A ragged batch gets all the slots of its waves,
+// and the device cuts the valid rows to fill them; unless whole sequences are one segment each and
+// nothing but that cut would need the sums of segments.
+rehyat::decay::Cut decay_cut(const DecayDims& a, bool ragged, bool last) {
+  rehyat::decay::Cut c{};
+  const bool bf16 = a.dt == REHYAT_BF16;
+  c.chunk = bf16 ? rehyat::decay::tc::kRows : rehyat::decay::kC;
+  const int start = bf16 ? 4 : 1;  // in quarters of a chunk
+  const int chunks = a.N > 0 ? (a.N + c.chunk - 1) / c.chunk : 1;
+  const long long BH = (long long)a.B * a.H;
+  long long best = -1, best_waves = 1;
   for (int n = 1; n <= chunks && n <= 256; ++n) {
     const int per = (chunks + n - 1) / n;
     if ((chunks + per - 1) / per != n) continue;  // the last ones would hold no rows
-    const long long waves = ((long long)BH * n + 147) / 148;
-    const long long cost = waves * (4 * per + start);
-    if (best_cost < 0 || cost < best_cost) {
-      best_cost = cost;
-      best = Segments{n, per * chunk};
+    const long long waves = (BH * n + 147) / 148, cost = waves * (4 * per + start);
+    if ((best < 0 || cost < best) && (n == 1 || (long long)a.B * n <= 65535)) {
+      best = cost;
+      best_waves = waves;
+      c.per_seq = n;
+      c.chunks = per;
     }
   }
-  return best;
+  c.slots = a.B * c.per_seq;
+  c.search = ragged && a.B <= rehyat::decay::kMaxSearch && (c.per_seq > 1 || last);
+  if (c.search) {
+    const long long fit = best_waves * 148 / a.H;
+    if (fit > c.slots) c.slots = (int)(fit < 65535 ? fit : 65535);
+  }
+  return c;
 }
 
 struct DecayPlan {
-  Segments seg;
+  rehyat::decay::Cut cut;
   size_t fwd, bwd, part[2], total;
 };
-DecayPlan plan_decay(const DecayDims& a, bool backward) {
+DecayPlan plan_decay(const DecayDims& a, bool backward, bool ragged, bool last) {
   DecayPlan p{};
   const size_t BH = (size_t)a.B * a.H;
-  p.seg = decay_segments((int)BH, a.N, a.dt);
+  p.cut = decay_cut(a, ragged, last);
   Carve cv;
-  const size_t states = BH * p.seg.n * a.D * a.D * 4;
+  const size_t states = (size_t)p.cut.slots * a.H * a.D * a.D * 4;
   p.fwd = cv.take(states);
   if (backward) {
     p.bwd = cv.take(states);
@@ -181,7 +189,7 @@ int launch_f32_rows(const rehyat::decay::Passes& a, dim3 grid, bool behind_scan,
 
 // The passes of one launch: the states they need, and the rows.
 int launch_decay_states(const Pass* p, int n, rehyat_dtype dt, cudaStream_t st) {
-  const dim3 grid(p[0].nseg, p[0].B * p[0].H, n);
+  const dim3 grid(p[0].H, p[0].cut.slots, n);
   if (dt == REHYAT_BF16) {
     using namespace rehyat::decay::tc;
     StatesArgs a{};
@@ -208,7 +216,7 @@ int launch_decay_states(const Pass* p, int n, rehyat_dtype dt, cudaStream_t st) 
 
 // behind_scan: the launch before is this call's scan, whose prefixes the kernel waits for.
 int launch_decay_rows(const Pass* p, int n, rehyat_dtype dt, bool behind_scan, cudaStream_t st) {
-  const dim3 grid(p[0].nseg, p[0].B * p[0].H, n);
+  const dim3 grid(p[0].H, p[0].cut.slots, n);
   if (dt == REHYAT_F32) {
     using namespace rehyat::decay;
     Passes a{};
@@ -238,29 +246,27 @@ int launch_decay_rows(const Pass* p, int n, rehyat_dtype dt, bool behind_scan, c
 }
 
 // The state before every segment of n <= 2 passes (rows b, c; time direction and e as in each) from
-// S0[i] (or zero), and the state after the last into last[i] unless null.  Sets each pass's prefix,
-// null for zero.  *scanned: whether a scan was launched.
+// S0[i] (or zero), and the state after the last into last[i] unless null.  *scanned: whether a scan
+// was launched.
 int decay_prefixes(Pass* p, int n, rehyat_dtype dt, const float* const* S0, float* const* last,
                    bool* scanned, cudaStream_t st) {
-  const bool many = p[0].nseg > 1;
+  const bool many = p[0].cut.per_seq > 1 || p[0].cut.search;
   Pass need[2];
   rehyat::decay::Scans a{};
   int sums = 0, scans = 0;
   for (int i = 0; i < n; ++i) {
-    const bool carried = many || S0[i];
-    p[i].prefix = carried ? p[i].delta : nullptr;
+    p[i].carried = many || S0[i];
     p[i].exact = last[i] != nullptr;
-    p[i].seg_skip = last[i] ? -1 : (p[i].reverse ? 0 : p[i].nseg - 1);
     if (many || last[i]) need[sums++] = p[i];
-    if (carried || last[i])
-      a.s[scans++] = rehyat::decay::Scan{p[i].delta, S0[i], last[i], p[i].reverse, carried};
+    if (p[i].carried || last[i])
+      a.s[scans++] = rehyat::decay::Scan{p[i].states, S0[i], last[i], p[i].reverse};
   }
   *scanned = scans > 0;
   if (scans == 0) return REHYAT_OK;
   const bool summed = sums > 0 && p[0].N > 0;
   if (summed) RH_TRY(launch_decay_states(need, sums, dt, st));
   a.log_decay = p[0].log_decay; a.lengths = p[0].lengths;
-  a.H = p[0].H; a.N = p[0].N; a.D = p[0].D; a.nseg = p[0].nseg; a.seg_rows = p[0].seg_rows;
+  a.B = p[0].B; a.H = p[0].H; a.N = p[0].N; a.D = p[0].D; a.cut = p[0].cut;
   const int n4 = a.D * a.D / 4;
   Behind l(dim3((n4 + 255) / 256, p[0].B * p[0].H, scans), 256, 0, st, summed);
   return cuda_check(cudaLaunchKernelEx(&l.cfg, rehyat::decay::decay_scan_kernel, a),
@@ -268,13 +274,13 @@ int decay_prefixes(Pass* p, int n, rehyat_dtype dt, const float* const* S0, floa
 }
 
 Pass decay_pass(const DecayDims& a, const float* log_decay, const int* lengths,
-                const Segments& s) {
+                const rehyat::decay::Cut& cut, void* states) {
   Pass p{};
   p.log_decay = log_decay;
   p.lengths = lengths;
   p.B = a.B; p.H = a.H; p.N = a.N; p.D = a.D;
-  p.nseg = s.n; p.seg_rows = s.rows;
-  p.seg_skip = -1;
+  p.cut = cut;
+  p.states = static_cast<float*>(states);
   p.sp = p.si = p.sd = 1.f;
   return p;
 }
@@ -379,9 +385,9 @@ int rehyat_decay_workspace_size(int B, int H, int Hk, int N, int D, int backward
   DecayDims d{B, H, Hk, N, D, REHYAT_BF16, 1.f};
   RH_TRY(check_decay(d));
   if (!bytes) return fail(REHYAT_ERR_ARG, "null pointer");
-  *bytes = plan_decay(d, backward != 0).total;
+  *bytes = plan_decay(d, backward != 0, true, true).total;  // the most of every kind of call
   d.dt = REHYAT_F32;
-  const size_t f32 = plan_decay(d, backward != 0).total;
+  const size_t f32 = plan_decay(d, backward != 0, true, true).total;
   if (f32 > *bytes) *bytes = f32;
   return REHYAT_OK;
 }
@@ -399,17 +405,16 @@ int rehyat_decay_forward(const rehyat_decay_forward_args* args, void* stream) {
   RH_TRY(check_rows("out", a.out, d, a.H));
   RH_TRY(check_states("S0", a.S0));
   RH_TRY(check_states("S_last", a.S_last));
-  const DecayPlan pl = plan_decay(d, false);
+  const DecayPlan pl = plan_decay(d, false, a.lengths != nullptr, a.S_last != nullptr);
   RH_TRY(check_scratch(pl, a.workspace, a.ws_bytes));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int group = a.H / a.Hk;
-  Pass p = decay_pass(d, a.log_decay, a.lengths, pl.seg);
+  Pass p = decay_pass(d, a.log_decay, a.lengths, pl.cut, static_cast<uint8_t*>(a.workspace) + pl.fwd);
   p.a = rows_of(a.q, 1);
   p.b = rows_of(a.k, group);
   p.c = rows_of(a.v, group);
   p.e = 1;
   p.sp = p.si = a.scale;
-  p.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + pl.fwd);
   bool scanned;
   RH_TRY(decay_prefixes(&p, 1, d.dt, &a.S0, &a.S_last, &scanned, st));
   if (a.N == 0) return REHYAT_OK;
@@ -434,7 +439,7 @@ int rehyat_decay_backward(const rehyat_decay_backward_args* args, void* stream) 
   RH_TRY(check_states("S0", a.S0));
   RH_TRY(check_states("dS_last", a.dS_last));
   RH_TRY(check_states("dS0", a.dS0));
-  const DecayPlan pl = plan_decay(d, true);
+  const DecayPlan pl = plan_decay(d, true, a.lengths != nullptr, a.dS0 != nullptr);
   RH_TRY(check_scratch(pl, a.workspace, a.ws_bytes));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
@@ -444,14 +449,12 @@ int rehyat_decay_backward(const rehyat_decay_backward_args* args, void* stream) 
 
   // states of the prompt, forward in time, for dQ (read transposed); gradient of the state, sum of
   // scale * q dO^T backward in time, for dK (transposed) and dV
-  Pass s[2] = {decay_pass(d, a.log_decay, a.lengths, pl.seg),
-               decay_pass(d, a.log_decay, a.lengths, pl.seg)};
-  s[0].delta = reinterpret_cast<float*>(ws + pl.fwd);
+  Pass s[2] = {decay_pass(d, a.log_decay, a.lengths, pl.cut, ws + pl.fwd),
+               decay_pass(d, a.log_decay, a.lengths, pl.cut, ws + pl.bwd)};
   s[0].e = 1;
   s[0].b = rk;
   s[0].c = rv;
   s[0].sp = s[0].si = a.scale;
-  s[1].delta = reinterpret_cast<float*>(ws + pl.bwd);
   s[1].reverse = 1;
   s[1].b = rq;
   s[1].c = rdo;
