@@ -1,10 +1,16 @@
 // Linear attention with a decay per head on the tensor cores (bf16, D <= 128): the two passes of
 // decay.cuh over 128-row chunks.
 //
-// Bound by memory once the products run on tcgen05: a chunk of the row pass moves 128 KB (a, b, c
-// in, out) for four 128^3 products, 2,048 clk of a tensor pipe against about 5,600 clk of one SM's
-// share of HBM.  So the kernels aim at keeping loads in flight: one CTA per SM, two (rows) or three
-// (states) stages of whole chunks, and one warp for each thing that waits.
+// A chunk of the row pass moves 128 KB of HBM (a, b, c in, out) for four 128^3 products: 5,600 clk of
+// one SM's share of the measured copy rate against 2,048 clk of the tensor pipe.  What it comes to,
+// about 5,000 clk, is shared memory: operands that the products read from it (224 KB), the copies in
+// (96), the weighting of b (64), the state's copy (32) and the output's staging (64) are 480 KB, 3,840
+// clk at 128 bytes a clk.  The 480x832 5 s prompt (12 heads, 32,760 rows, D = 128): states 46 us
+// (4.4 TB/s), rows 74 us (5.4 TB/s).  Long runs are held at 1.45-1.65 GHz by the board's power limit.
+// Not faster: the outputs on eight warps of their own (setmaxnreg shares), runs of chunks that cross
+// from one head into the next, L2 eviction hints, waits by test_wait or with nanosleep.
+// One CTA per SM, two (rows) or three (states) stages of whole chunks, one warp for each thing that
+// waits, short loops (straight-line code of every role at once overran the instruction cache).
 //
 // Rounded to bf16: the weighted scores P, the weighted rows b of the carried state, the state the
 // rows read, and the output; sums, states and powers are fp32.  The states pass multiplies each
@@ -281,8 +287,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
 // Rows.
 // ---------------------------------------------------------------------------------------------
 // warps 0-7: scores and outputs, 8-15: weights and the state (of each, four warps take columns 0-63
-// and four 64-127), 16: copies in, 17: products, 18: copies out.  With four warps for each of the
-// first two the chains between the products took 8,800 clk a chunk, 5,600 more than the products.
+// and four 64-127), 16: copies in, 17: products, 18: copies out.
 constexpr int kRwThreads = 608;
 constexpr int kRwIn = 16, kRwMma = 17, kRwOut = 18;
 constexpr uint32_t kRwStage = 3 * kTile;

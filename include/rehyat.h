@@ -355,7 +355,10 @@ int rehyat_rotary(const rehyat_rotary_args* args, void* stream);
  * taken as within [0, N]; NULL: N):
  *   o_i = scale * ( sum_{j<=i} L^(i-j) (q_i . k_j) v_j  +  L^(i+1) q_i S_0 )
  *   S_n = L^n S_0 + sum_{j<n} L^(n-1-j) k_j v_j^T
- * Rows n .. N-1 are padding: never read into a result, and zero in every output.
+ * Rows n .. N-1 are padding: never read into a result, and zero in every output.  A NaN or an
+ * infinity in a row stays within its sequence and the heads that share its k and v; there it
+ * reaches the rows after it, the states, and earlier rows of its own chunk (128 rows in bf16, 64
+ * in fp32); in the gradients any row.
  * D a multiple of 8 up to 128; N may be 0.  bf16: tensor-core products with fp32 accumulation
  * (the states are summed from two-part products, to fp32 accuracy).  fp32: CUDA cores.
  * rehyat_decay_workspace_size: device scratch that the forward (backward = 0) or the gradients
