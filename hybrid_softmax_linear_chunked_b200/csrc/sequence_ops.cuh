@@ -4,6 +4,7 @@
 #pragma once
 
 #include <atomic>
+#include <initializer_list>
 
 #include "decay.cuh"
 #include "decay_bf16.cuh"
@@ -290,6 +291,13 @@ void set_out(Pass& p, const rehyat_rows& o) {
   p.ob = o.batch; p.oh = o.head; p.on = o.row;
 }
 
+// CTAs that share a row write their part of it while others may still read theirs.
+int check_apart(const char* what, const void* out, std::initializer_list<const void*> others) {
+  for (const void* p : others)
+    if (p && p == out) return fail(REHYAT_ERR_ARG, "%s may not be another argument", what);
+  return REHYAT_OK;
+}
+
 int check_states(const char* what, const float* S) {
   if (S && !aligned16(S)) return fail(REHYAT_ERR_ALIGN, "%s is not 16-byte aligned", what);
   return REHYAT_OK;
@@ -345,8 +353,17 @@ int rehyat_rotary(const rehyat_rotary_args* args, void* stream) {
     const long long st[6] = {t.xb, t.xh, t.xn, t.yb, t.yh, t.yn};
     const int size[3] = {a.B, t.heads, a.n};
     whole &= aligned16(t.x) && aligned16(t.y);
-    for (int j = 0; j < 6; ++j)
-      if (size[j % 3] > 1) whole &= (st[j] * el) % 16 == 0;
+    for (int j = 0; j < 6; ++j) {
+      if (size[j % 3] <= 1) continue;
+      whole &= (st[j] * el) % 16 == 0;
+      if (j >= 3 && st[j] < a.D)
+        return fail(REHYAT_ERR_ARG, "an output's stride %lld of a dimension of %d is below D=%d", st[j],
+                    size[j % 3], a.D);
+    }
+  }
+  if (a.Hk) {
+    RH_TRY(check_apart("q_out", a.q_out.p, {a.k.p, a.k_out.p}));
+    RH_TRY(check_apart("k_out", a.k_out.p, {a.q.p}));
   }
   p.B = a.B; p.n = a.n; p.D = a.D; p.R = a.R;
   p.interleaved = a.interleaved; p.copy_tail = !in_place && a.R < a.D;
@@ -407,6 +424,7 @@ int rehyat_decay_forward(const rehyat_decay_forward_args* args, void* stream) {
   RH_TRY(check_states("S_last", a.S_last));
   const DecayPlan pl = plan_decay(d, false, a.lengths != nullptr, a.S_last != nullptr);
   RH_TRY(check_scratch(pl, a.workspace, a.ws_bytes));
+  RH_TRY(check_apart("out", a.out.p, {a.q.p, a.k.p, a.v.p}));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int group = a.H / a.Hk;
   Pass p = decay_pass(d, a.log_decay, a.lengths, pl.cut, static_cast<uint8_t*>(a.workspace) + pl.fwd);
@@ -441,6 +459,10 @@ int rehyat_decay_backward(const rehyat_decay_backward_args* args, void* stream) 
   RH_TRY(check_states("dS0", a.dS0));
   const DecayPlan pl = plan_decay(d, true, a.lengths != nullptr, a.dS0 != nullptr);
   RH_TRY(check_scratch(pl, a.workspace, a.ws_bytes));
+  RH_TRY(check_apart("dq", a.dq.p, {a.q.p, a.k.p, a.v.p, a.dout.p}));
+  RH_TRY(check_apart("dk", a.dk.p, {a.q.p, a.k.p, a.v.p, a.dout.p, a.dq.p}));
+  RH_TRY(check_apart("dv", a.dv.p, {a.q.p, a.k.p, a.v.p, a.dout.p, a.dq.p, a.dk.p}));
+  RH_TRY(check_apart("dS0", a.dS0, {a.S0, a.dS_last}));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const int group = a.H / a.Hk;
@@ -515,6 +537,7 @@ int rehyat_decay_step(const rehyat_decay_step_args* args, void* stream) {
   RH_TRY(check_states("state", a.state));
   if (a.pool < 1 || (!a.slots && a.pool < a.B))
     return fail(REHYAT_ERR_ARG, "a pool of %d states for %d sequences", a.pool, a.B);
+  RH_TRY(check_apart("out", a.out.p, {a.q.p, a.k.p, a.v.p}));
   rehyat::decay::StepParams p{};
   const int group = a.H / a.Hk;
   p.q = rows_of(a.q, 1);

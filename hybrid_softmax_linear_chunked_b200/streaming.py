@@ -94,9 +94,10 @@ class DecayStream:
     going on from the states the calls before left (decay_forward and decay_step of the binding),
     with rotary positions on q and k counted per sequence.
 
-    The session owns the states [B,H,D,D] fp32, the number of rows each sequence has seen ([B]
-    int32 on the device, so ragged prompts and captured steps need no host value) and a workspace
-    that grows with the longest prompt.  Memory does not grow with the rows seen.
+    The session owns the states [B,H,D,D] fp32 and the number of rows each sequence has seen ([B]
+    int32 on the device, so ragged prompts and captured calls need no host value).  Memory does not
+    grow with the rows seen.  Scratch is allocated by each prompt: one kept here would be replaced
+    by a longer prompt's while a captured prompt still writes to it.
 
     log_decay [H] fp32; Hk key/value heads (default H); scale defaults to D ** -0.5.  freq (fp64
     [R/2], see rotary_frequencies) turns on rotary positions; rotary_scale and interleaved as in
@@ -114,7 +115,6 @@ class DecayStream:
         dev = log_decay.device
         self.state = torch.zeros(B, self.H, D, D, dtype=torch.float32, device=dev)
         self.seen = torch.zeros(B, dtype=torch.int32, device=dev)
-        self.workspace = None
 
     def reset(self) -> None:
         """Start new sequences (the buffers are kept)."""
@@ -138,14 +138,10 @@ class DecayStream:
         """Outputs [B,H,N,D] of the next N rows of every sequence, or of the first lengths[b]
         (int32 [B] on the device, 0 .. N) of a padded batch, whose other rows are zero."""
         self._check(q, k, v)
-        B, H, N, D = q.shape
-        need = rb.decay_workspace_size(B, H, self.Hk, N, D)
-        if self.workspace is None or self.workspace.numel() < need:
-            self.workspace = torch.empty(need, dtype=torch.uint8, device=self.state.device)
+        N = q.shape[2]
         q, k = self._turn(q, k)
         out, _ = rb.decay_forward(q, k, v, self.log_decay, scale=self.scale, lengths=lengths,
-                                  state=self.state, final_state=self.state,
-                                  workspace=self.workspace)
+                                  state=self.state, final_state=self.state)
         self.seen += N if lengths is None else lengths.clamp(0, N)
         return out
 

@@ -331,7 +331,7 @@ typedef struct {
  *         pos64 != 0), to which `start` and, with add_index != 0, i are added; pos NULL: 0.
  * Angles are exact modulo a turn for every 64-bit position.  Any even 2 <= R <= D; no alignment
  * or stride rule beyond the element's (16-byte aligned rows with R, D multiples of 16 move whole
- * vectors).  q_out/k_out may be q/k (same strides); then nothing is copied.  Enqueued on `stream`;
+ * vectors; an input may be expanded, an output not).  q_out/k_out may be q/k (same strides); then nothing is copied.  Enqueued on `stream`;
  * allocates nothing. */
 typedef struct {
   int B, n, Hq, Hk, D, R;
@@ -359,7 +359,7 @@ int rehyat_rotary(const rehyat_rotary_args* args, void* stream);
  * infinity in a row stays within its sequence and the heads that share its k and v; there it
  * reaches the rows after it, the states, and earlier rows of its own chunk (128 rows in bf16, 64
  * in fp32); in the gradients any row.
- * D a multiple of 8 up to 128; N may be 0.  bf16: tensor-core products with fp32 accumulation
+ * D a multiple of 8 up to 128; B*H up to 65535; N may be 0.  bf16: tensor-core products with fp32 accumulation
  * (the states are summed from two-part products, to fp32 accuracy).  fp32: CUDA cores.
  * rehyat_decay_workspace_size: device scratch that the forward (backward = 0) or the gradients
  * need for these sizes. */

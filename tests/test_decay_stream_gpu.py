@@ -108,6 +108,27 @@ def test_resume_and_captured_steps_give_the_same_bits(dev):
     assert not again.state.any() and not again.seen.any()
 
 
+def test_captured_prompt_beside_a_longer_one(dev):
+    """A captured prompt writes only to memory it owns, also after a longer prompt of the session."""
+    g = torch.Generator().manual_seed(3)
+    short, other, long = [rows(g, dev, torch.bfloat16, n) for n in (300, 300, 2500)]
+    sess, plain = session(dev), session(dev)
+    sess.prompt(*short)
+    x = [t.clone() for t in short]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = sess.prompt(*x)
+    sess.prompt(*long)
+    fill = [torch.full((1 << 18,), i, dtype=torch.int32, device=dev) for i in range(32)]
+    for t, s in zip(x, other):
+        t.copy_(s)
+    graph.replay()
+    want = [plain.prompt(*y) for y in (short, long, other)][-1]
+    assert torch.equal(out, want) and torch.equal(sess.state, plain.state)
+    assert torch.equal(sess.seen, plain.seen)
+    assert all(bool((t == i).all()) for i, t in enumerate(fill))
+
+
 def test_refuses(dev):
     g = torch.Generator().manual_seed(2)
     sess = session(dev)

@@ -72,6 +72,45 @@ def test_decay_step_refuses(lib, kw, status):
     assert decay(lib, "step", **kw) == status
 
 
+def test_written_tensors_are_no_other_argument(lib):
+    """Refused with the message that says so; out of the way of every input's own checks."""
+    at = lambda heads, i: rows(heads, FAKE + (i << 16))  # noqa: E731
+    apart = dict(q=at(H, 1), k=at(HK, 2), v=at(HK, 3), out=at(H, 4), dout=at(H, 5), dq=at(H, 6),
+                 dk=at(HK, 7), dv=at(HK, 8), S0=FAKE + (9 << 16), dlast=FAKE + (10 << 16))
+    for call, pairs in (("forward", ["out q", "out k", "out v"]),
+                        ("step", ["out q", "out k", "out v"]),
+                        ("backward", ["dq q", "dq dout", "dk k", "dk v", "dk dq", "dv v", "dv dk",
+                                      "dS0 S0", "dS0 dlast"])):
+        for pair in pairs:
+            w, r = pair.split()
+            kw = dict(apart, **{w: (apart[r][0],) + apart[w][1:] if w != "dS0" else apart[r]})
+            assert decay(lib, call, **kw) == -1
+            assert lib.rehyat_last_error().decode().endswith("may not be another argument"), pair
+
+
+def rotary_status(lib, **kw):
+    a = dict(B=B, n=N, Hq=H, Hk=HK, D=D, R=D, interleaved=0, inverse=0, axes=1, pos64=0,
+             add_index=1, dtype=rb.REHYAT_BF16, pos_axis=0, pos_batch=0, pos_token=0, start=0,
+             freq=FAKE, axis=0, pos=0, q=rows(H, FAKE), k=rows(HK, FAKE + (1 << 16)),
+             q_out=rows(H, FAKE + (2 << 16)), k_out=rows(HK, FAKE + (3 << 16)), scale=1.0)
+    a.update(kw)
+    flat = [y for x in a.values() for y in (x if isinstance(x, tuple) else (x,))]
+    return lib.rehyat_rotary(rb._ROTARY.pack(*flat), None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q_out=rows(H, FAKE + (1 << 16))), dict(q_out=rows(H, FAKE + (3 << 16))),
+    dict(k_out=rows(HK, FAKE)),
+    dict(k_out=(FAKE + (3 << 16), HK * N * D, 0, D)),   # the output's heads expanded
+    dict(q_out=(FAKE + (2 << 16), 0, N * D, D)),
+    dict(k=(FAKE + (1 << 16), HK * N * D, 0, D),        # expanded and in place
+         k_out=(FAKE + (1 << 16), HK * N * D, 0, D)),
+])
+def test_rotary_refuses_outputs_that_overlap(lib, kw):
+    assert rotary_status(lib, **kw) == -1
+    assert lib.rehyat_last_error().decode()
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(B=0), -1), (dict(n=-1), -1), (dict(Hq=0), -1), (dict(Hk=-1), -1), (dict(R=0), -2),
     (dict(R=7), -2), (dict(R=66), -2), (dict(axes=0), -1), (dict(axes=5), -1),
