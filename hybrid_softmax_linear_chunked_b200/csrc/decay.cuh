@@ -231,13 +231,13 @@ __device__ __forceinline__ uint64_t twice(float x) { return sm100::f2_pack(x, x)
 
 // Rows [r0, r0 + kC) of one head into shared memory, columns [D, kDp) and rows at or past `end` as
 // zeros whatever the tensor holds there.
-template <int kDp>
+template <int kDp, int kFrom = kThreads>
 __device__ __forceinline__ void load_rows(float* dst, const Rows& t, int b, int h, int r0, int end,
                                           int D) {
   const float* src = static_cast<const float*>(t.p) + b * t.sb + (h / t.group) * t.sh;
   constexpr int v4 = kDp / 4;
 #pragma unroll
-  for (int i0 = 0; i0 < kC * v4; i0 += kThreads) {
+  for (int i0 = 0; i0 < kC * v4; i0 += kFrom) {
     const int i = i0 + threadIdx.x, r = i / v4, c = (i % v4) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r0 + r < end && c < D) x = load4<float>(src + (long long)(r0 + r) * t.sn + c);
@@ -251,7 +251,7 @@ template <int kDp>
 __device__ __forceinline__ void outer_add(uint64_t (&acc)[kDp / 16][kDp / 32], const float* x,
                                           const float* y, const float* w, int rows) {
   constexpr int n = kDp / 32, ld = kDp + 4;
-  const int i0 = (threadIdx.x / 16) * 2, j0 = (threadIdx.x % 16) * 2;
+  const int t = threadIdx.x % kThreads, i0 = (t / 16) * 2, j0 = (t % 16) * 2;
 #pragma unroll 2
   for (int r = 0; r < rows; ++r) {
     const uint64_t wr = twice(w[r]);
@@ -409,18 +409,27 @@ __device__ __forceinline__ void zero_padding(const Pass& p, int t, int n) {
   }
 }
 
-// The rows of one segment: chunks of kC in time order, the state carried in shared memory.
-// Bound by the fp32 pipes: kC D (kC + kC / 2 + 2 D) multiply-adds a chunk.
-// grid (H, slots, passes), block 256.
+// The rows of one segment: chunks of kC in time order.  Bound by the fp32 pipes and shared memory
+// alike: about kC D (1.1 kC + 2 D) multiply-adds a chunk, 56 % of the fp32 rate with 60 % of the
+// shared-memory cycles at D = 128.  Half of the warps form scores and outputs, the other half the
+// state, which they hold in registers and copy out between chunks (gradients of 4 sequences, 6 heads
+// over 3, 1,151 rows, D = 128: 250 us, 281 with eight warps going through all of it in turn).
+// Narrow heads run two CTAs an SM on 64 registers a thread, wide ones one on 128.
+// grid (H, slots, passes), block 512.
+constexpr int kRowThreads = 2 * kThreads;
+template <int kN>
+struct Blocks {
+  static constexpr int value = kN;
+};
 template <int kDp>
-__global__ void __launch_bounds__(kThreads, kDp <= 64 ? 2 : 1)
+__global__ void __launch_bounds__(kRowThreads, kDp <= 64 ? 2 : 1)
     decay_rows_kernel(const __grid_constant__ Passes all) {
   extern __shared__ __align__(16) float smf[];
   const Pass& p = all.p[blockIdx.z];
   const Segment seg = find_segment(p);
   const int b = seg.b, h = seg.h, r_begin = seg.begin, r_end = seg.end;
-  zero_padding<4>(p, threadIdx.x, kThreads);
-  constexpr int n = kDp / 32, ld = kDp + 4, ldp = kC + 4;
+  zero_padding<4>(p, threadIdx.x, kRowThreads);
+  constexpr int n = kDp / 32, ld = kDp + 4, ldp = kC + 4, kScoreSteps = kDp <= 64 ? 1 : 4;
   float* sa = smf;
   float* sb = sa + kC * ld;
   float* sc = sb + kC * ld;
@@ -428,14 +437,14 @@ __global__ void __launch_bounds__(kThreads, kDp <= 64 ? 2 : 1)
   float* ss = sp + kC * ldp;
   float* spow = ss + kDp * ld;  // sp L^d
   float* sw = spow + kC;        // weights of b's rows
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = (tid >> 5) & 7;
+  const bool states = tid >= kThreads;
   const float g2 = log2_decay(p.log_decay, h);
-  float* out = static_cast<float*>(p.out) + b * p.ob + h * p.oh;
   if (tid < kC) spow[tid] = p.sp * exp2f(g2 * (float)tid);
 
   sm100::grid_dep_wait();  // the states come from the launch before
   if (r_begin >= r_end) return;
-  for (int i = tid; i < kDp * (kDp / 4); i += kThreads) {
+  for (int i = tid; i < kDp * (kDp / 4); i += kRowThreads) {
     const int r = i % kDp, c = (i / kDp) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (p.carried && r < p.D && c < p.D) {
@@ -450,109 +459,146 @@ __global__ void __launch_bounds__(kThreads, kDp <= 64 ? 2 : 1)
     *reinterpret_cast<float4*>(ss + r * ld + c) = x;
   }
   const int nc = (r_end - r_begin + kC - 1) / kC;
-  const int i4 = (tid / 16) * 4, j2 = (tid % 16) * 2;  // rows i4 .. i4 + 3, column pairs from j2
-  for (int ci = 0; ci < nc; ++ci) {
-    const int r0 = r_begin + (p.reverse ? nc - 1 - ci : ci) * kC;
-    const int rows = min(r_end - r0, kC);  // valid rows
-    __syncthreads();
-    load_rows<kDp>(sa, p.a, b, h, r0, r_end, p.D);
-    load_rows<kDp>(sb, p.b, b, h, r0, r_end, p.D);
-    load_rows<kDp>(sc, p.c, b, h, r0, r_end, p.D);
-    if (tid < kC)
+  auto chunk = [&](int ci) { return r_begin + (p.reverse ? nc - 1 - ci : ci) * kC; };
+  auto load = [&](int r0) {
+    load_rows<kDp, kRowThreads>(sa, p.a, b, h, r0, r_end, p.D);
+    load_rows<kDp, kRowThreads>(sb, p.b, b, h, r0, r_end, p.D);
+    load_rows<kDp, kRowThreads>(sc, p.c, b, h, r0, r_end, p.D);
+    if (tid < kC) {
+      const int rows = min(r_end - r0, kC);
       sw[tid] = p.sd * exp2f(g2 * (float)(p.reverse ? tid + 1 - p.e : rows - p.e - tid));
-    __syncthreads();
-    {  // P = sp * L^|i-j| (a_i . b_j) over the past of i, 4 x 4 a thread (columns 16 apart)
-      const int j0 = tid % 16;
-      float acc[4][4] = {};
-#pragma unroll 4
-      for (int k = 0; k < kDp; k += 4) {
-        float4 x[4], y[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          x[u] = *reinterpret_cast<const float4*>(sa + (i4 + u) * ld + k);
-          y[u] = *reinterpret_cast<const float4*>(sb + (j0 + 16 * u) * ld + k);
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int w = 0; w < 4; ++w)
-            acc[u][w] = fmaf(x[u].x, y[w].x, fmaf(x[u].y, y[w].y,
-                        fmaf(x[u].z, y[w].z, fmaf(x[u].w, y[w].w, acc[u][w]))));
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const int i = i4 + u, j = j0 + 16 * w, d = p.reverse ? j - i : i - j;
-          sp[i * ldp + j] = d >= 0 && j < rows ? spow[max(d, 0)] * acc[u][w] : 0.f;
-        }
     }
-    __syncthreads();
-    {  // out = si * L^(t + e) a^T S + P c
-      uint64_t acc[4][n];
+  };
+  load(chunk(0));
+  __syncthreads();
+  auto both = [] { sm100::named_bar_sync(1, kRowThreads); };  // of both halves, from either's code
+  if (states) {  // S = L^rows S + sd * sum L^(rows - t - e) b c^T
+    const int i2 = ((tid - kThreads) / 16) * 2, j2 = (tid % 16) * 2;
+    uint64_t acc[2 * n][n];
+    auto at = [&](int i, int v) {
+      return reinterpret_cast<uint64_t*>(ss + (i2 + 32 * (i / 2) + (i & 1)) * ld + j2 + 32 * v);
+    };
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+    for (int i = 0; i < 2 * n; ++i)
 #pragma unroll
-        for (int v = 0; v < n; ++v) acc[u][v] = 0ull;
-      auto add = [&](const float* xr, int ldx, const float* y, int k0, int k1) {
-#pragma unroll 2
-        for (int k = k0; k < k1; k += 4) {
-          float4 x[4];
+      for (int v = 0; v < n; ++v) acc[i][v] = *at(i, v);
+    for (int ci = 0; ci < nc; ++ci) {
+      const int rows = min(r_end - chunk(ci), kC);
+      const bool more = ci + 1 < nc;
+      if (more) {
+        const uint64_t keep = twice(exp2f(g2 * (float)rows));
 #pragma unroll
-          for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const float4*>(xr + (i4 + u) * ldx + k);
+        for (int i = 0; i < 2 * n; ++i)
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint64_t yv[n];
-#pragma unroll
-            for (int v = 0; v < n; ++v) yv[v] = pair_at(y + (k + w) * ld + j2 + 32 * v);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const float xv = w == 0 ? x[u].x : w == 1 ? x[u].y : w == 2 ? x[u].z : x[u].w;
-#pragma unroll
-              for (int v = 0; v < n; ++v) acc[u][v] = sm100::f2_fma(twice(xv), yv[v], acc[u][v]);
-            }
-          }
-        }
-      };
-      add(sa, ld, ss, 0, kDp);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int t = p.reverse ? rows - 1 - (i4 + u) : i4 + u;
-        const uint64_t f = twice(p.si * exp2f(g2 * (float)(max(t, 0) + p.e)));
-#pragma unroll
-        for (int v = 0; v < n; ++v) acc[u][v] = sm100::f2_mul(f, acc[u][v]);
+          for (int v = 0; v < n; ++v) acc[i][v] = sm100::f2_mul(keep, acc[i][v]);
+        outer_add<kDp>(acc, sb, sc, sw, rows);
       }
-      // a warp's eight rows have no past beyond their last (first, backward in time)
-      add(sp, ldp, sc, p.reverse ? warp * 8 : 0, p.reverse ? kC : warp * 8 + 8);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int r = i4 + u;
-        if (r0 + r >= p.N) continue;
-        float* dst = out + (long long)(r0 + r) * p.on;
-#pragma unroll
-        for (int v = 0; v < n; ++v)
-          if (j2 + 32 * v < p.D)
-            *reinterpret_cast<uint64_t*>(dst + j2 + 32 * v) = r < rows ? acc[u][v] : 0ull;
-      }
-    }
-    __syncthreads();
-    if (ci + 1 < nc) {  // S = L^rows S + sd * sum L^(rows - t - e) b c^T
-      const uint64_t keep = twice(exp2f(g2 * (float)rows));
-      const int i2 = (tid / 16) * 2;
-      uint64_t acc[2 * n][n];
-      auto at = [&](int i, int v) {
-        return reinterpret_cast<uint64_t*>(ss + (i2 + 32 * (i / 2) + (i & 1)) * ld + j2 + 32 * v);
-      };
-#pragma unroll
-      for (int i = 0; i < 2 * n; ++i)
-#pragma unroll
-        for (int v = 0; v < n; ++v) acc[i][v] = sm100::f2_mul(keep, *at(i, v));
-      outer_add<kDp>(acc, sb, sc, sw, rows);
+      both();  // the chunk is used up
+      if (!more) break;
 #pragma unroll
       for (int i = 0; i < 2 * n; ++i)
 #pragma unroll
         for (int v = 0; v < n; ++v) *at(i, v) = acc[i][v];
+      load(chunk(ci + 1));
+      both();
     }
+    return;
+  }
+  float* out = static_cast<float*>(p.out) + b * p.ob + h * p.oh;
+  // Eight rows a warp, of which a thread has rows i4 .. i4 + 3 and column pairs from j2.  The cost of a
+  // warp's past grows with its rows, so the two warps of a scheduler (w, w + 4) get rows that
+  // even out.
+  const int eight = (warp < 4 ? warp : 11 - warp) * 8;
+  const int i4 = eight + ((tid / 16) & 1) * 4, j2 = (tid % 16) * 2;
+  // P = sp * L^|i-j| (a_i . b_j) over the past of i, 4 x kBlocks a thread (columns 16 apart)
+  auto scores = [&](auto blocks, int rows) {
+    constexpr int kBlocks = decltype(blocks)::value;
+    const int j0 = tid % 16 + (p.reverse ? kC - 16 * kBlocks : 0);
+    float acc[4][kBlocks] = {};
+#pragma unroll kScoreSteps
+    for (int k = 0; k < kDp; k += 4) {
+      float4 x[4], y[kBlocks];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const float4*>(sa + (i4 + u) * ld + k);
+#pragma unroll
+      for (int w = 0; w < kBlocks; ++w)
+        y[w] = *reinterpret_cast<const float4*>(sb + (j0 + 16 * w) * ld + k);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int w = 0; w < kBlocks; ++w)
+          acc[u][w] = fmaf(x[u].x, y[w].x, fmaf(x[u].y, y[w].y,
+                      fmaf(x[u].z, y[w].z, fmaf(x[u].w, y[w].w, acc[u][w]))));
+    }
+    __syncwarp();  // a warp's rows of P are its own: it has read the last chunk's
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int w = 0; w < kBlocks; ++w) {
+        const int i = i4 + u, j = j0 + 16 * w, d = p.reverse ? j - i : i - j;
+        sp[i * ldp + j] = d >= 0 && j < rows ? spow[max(d, 0)] * acc[u][w] : 0.f;
+      }
+  };
+  for (int ci = 0; ci < nc; ++ci) {
+    const int r0 = chunk(ci), rows = min(r_end - r0, kC);  // valid rows
+    const int past = p.reverse ? 4 - eight / 16 : eight / 16 + 1;  // blocks of 16 columns
+    switch (past) {
+      case 1: scores(Blocks<1>{}, rows); break;
+      case 2: scores(Blocks<2>{}, rows); break;
+      case 3: scores(Blocks<3>{}, rows); break;
+      default: scores(Blocks<4>{}, rows); break;
+    }
+    __syncwarp();
+    // out = si * L^(t + e) a^T S + P c
+    uint64_t acc[4][n];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int v = 0; v < n; ++v) acc[u][v] = 0ull;
+    auto add = [&](const float* xr, int ldx, const float* y, int k0, int k1) {
+#pragma unroll 2
+      for (int k = k0; k < k1; k += 4) {
+        float4 x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const float4*>(xr + (i4 + u) * ldx + k);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint64_t yv[n];
+#pragma unroll
+          for (int v = 0; v < n; ++v) yv[v] = pair_at(y + (k + w) * ld + j2 + 32 * v);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float xv = w == 0 ? x[u].x : w == 1 ? x[u].y : w == 2 ? x[u].z : x[u].w;
+#pragma unroll
+            for (int v = 0; v < n; ++v) acc[u][v] = sm100::f2_fma(twice(xv), yv[v], acc[u][v]);
+          }
+        }
+      }
+    };
+    add(sa, ld, ss, 0, kDp);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int t = p.reverse ? rows - 1 - (i4 + u) : i4 + u;
+      const uint64_t f = twice(p.si * exp2f(g2 * (float)(max(t, 0) + p.e)));
+#pragma unroll
+      for (int v = 0; v < n; ++v) acc[u][v] = sm100::f2_mul(f, acc[u][v]);
+    }
+    // a warp's eight rows have no past beyond their last (first, backward in time)
+    add(sp, ldp, sc, p.reverse ? eight : 0, p.reverse ? kC : eight + 8);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = i4 + u;
+      if (r0 + r >= p.N) continue;
+      float* dst = out + (long long)(r0 + r) * p.on;
+#pragma unroll
+      for (int v = 0; v < n; ++v)
+        if (j2 + 32 * v < p.D)
+          *reinterpret_cast<uint64_t*>(dst + j2 + 32 * v) = r < rows ? acc[u][v] : 0ull;
+    }
+    both();  // the chunk is used up
+    if (ci + 1 == nc) break;
+    load(chunk(ci + 1));
+    both();
   }
 }
 

@@ -182,9 +182,14 @@ int launch_f32_states(const rehyat::decay::Passes& a, dim3 grid, cudaStream_t st
 template <int kDp>
 int launch_f32_rows(const rehyat::decay::Passes& a, dim3 grid, bool behind_scan, cudaStream_t st) {
   using namespace rehyat::decay;
-  const int smem = rows_smem_floats(kDp) * 4;
-  RH_TRY(allow_smem<decay_rows_kernel<kDp>>(smem));
-  Behind l(grid, kThreads, smem, st, behind_scan);
+  // A grid of one wave asks for more than half of an SM's shared memory: where two CTAs of a narrow
+  // head fit one SM, those that start while the scan still runs would pair up on the SMs it has left
+  // (4 sequences, 6 heads, 1,151 rows, D = 64: 59.6 us, 43.6 spread out).
+  constexpr int kNeeds = rows_smem_floats(kDp) * 4, kAlone = 116 << 10;
+  constexpr int kMost = kNeeds > kAlone ? kNeeds : kAlone;
+  const int smem = (long long)grid.x * grid.y * grid.z <= 148 ? kMost : kNeeds;
+  RH_TRY(allow_smem<decay_rows_kernel<kDp>>(kMost));
+  Behind l(grid, kRowThreads, smem, st, behind_scan);
   return cuda_check(cudaLaunchKernelEx(&l.cfg, decay_rows_kernel<kDp>, a), "decay rows launch");
 }
 
