@@ -353,6 +353,36 @@ def test_calls_repeat_bit_for_bit_and_replay_from_graphs(dev):
             assert torch.equal(x, y)
 
 
+def test_calls_at_once(dev):
+    """Calls on three streams, not ordered to one another, give what they give one by one."""
+    shapes = [(torch.bfloat16, 2, 6, 3, 2000, 128), (torch.bfloat16, 1, 3, 3, 3000, 64),
+              (torch.float32, 2, 4, 2, 500, 64)]
+    probs = [problem(dev, dt, B, H, Hk, N, D, True, seed=30 + i)
+             for i, (dt, B, H, Hk, N, D) in enumerate(shapes)]
+    lengths = [torch.tensor([N // 3, N][:B], dtype=torch.int32, device=dev)
+               for _, B, _, _, N, _ in shapes]
+
+    def calls(i):
+        p, kw = probs[i], dict(scale=0.1, lengths=lengths[i])
+        x = (p["q"], p["k"], p["v"], p["g"])
+        out, S = rb.decay_forward(*x, state=p["S0"], final_state=True, **kw)
+        return [out, S, *rb.decay_backward(*x, p["dout"], state=p["S0"], dfinal=S, **kw).values()]
+
+    want = [calls(i) for i in range(3)]
+    torch.cuda.synchronize(dev)
+    streams = [torch.cuda.Stream(dev) for _ in shapes]
+    got = [[] for _ in shapes]
+    for _ in range(4):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(calls(i))
+    torch.cuda.synchronize(dev)
+    rb.sync_status(dev)
+    for w, runs in zip(want, got):
+        for run in runs:
+            assert all(torch.equal(x, y) for x, y in zip(w, run))
+
+
 def test_refuses(dev):
     p = problem(dev, torch.bfloat16, 2, 4, 2, 16, 64, True)
     q, k, v, g = (p[x] for x in ("q", "k", "v", "g"))
