@@ -72,12 +72,32 @@ __device__ __forceinline__ uint4 scale8(uint4 x, float w, uint4& lo) {
   lo = make_uint4(rest[0], rest[1], rest[2], rest[3]);
   return make_uint4(hi[0], hi[1], hi[2], hi[3]);
 }
-// Eight bf16 values times a bf16 weight.
-__device__ __forceinline__ uint4 mul8(uint4 x, __nv_bfloat162 w) {
+// A weight w > 0 in two bf16 parts, hi + lo, good to 2^-16 of w.  hi is cut, so lo has its sign, and
+// lo is never zero: an infinity times the parts stays one.
+struct Weight {
+  __nv_bfloat162 hi, lo;
+  __device__ __forceinline__ explicit Weight(float w) {
+    const float h = __uint_as_float(__float_as_uint(w) & 0xffff0000u);
+    hi = __float2bfloat162_rn(h);
+    lo = __float2bfloat162_rn(fmaxf(w - h, 1.17549435e-38f));
+  }
+};
+// Eight bf16 values times a weight, rounded to bf16 once: the small part's product is added to the
+// large one's before that is rounded.
+__device__ __forceinline__ uint4 mul8(uint4 x, const Weight& w) {
   __nv_bfloat162* v = reinterpret_cast<__nv_bfloat162*>(&x);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = __hmul2(v[i], w);
+  for (int i = 0; i < 4; ++i) v[i] = __hfma2(v[i], w.hi, __hmul2(v[i], w.lo));
   return x;
+}
+// Weights L^m of n rows, m from 1 - e to n - e, are taken relative to L^middle, which a sum over the
+// rows is multiplied by in fp32.  Rounding x w to bf16 gives x for every w just below 1: where the
+// decay is slow, all rows would be rounded up together and their sum come out up to 0.1 % too large
+// (measured 0.08 % at log_decay = -1.2e-5; 0.002 % with w on both sides of 1).  A span beyond two
+// halvings crosses enough steps of the type to average out by itself, and is left alone so that no
+// power grows beyond 2.
+__device__ __forceinline__ float middle(float g2, int n, int e) {
+  return fabsf(g2) * (float)(n + 1) <= 2.f ? 0.5f * (float)(n + 1) - (float)e : 0.f;
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -91,7 +111,8 @@ constexpr uint32_t kStOffLo = kStStages * 2 * kTile;
 constexpr uint32_t kStSmem = kStOffLo + kTile + 1024;
 static_assert(kStSmem + 1024 <= 232448, "shared memory over the limit");
 
-// Every weight is taken to the segment's end, so chunks add up without rescaling, in any order.
+// Every weight is taken to the segment's end (or its middle, see above), so chunks add up without
+// rescaling, in any order; what all share, that power and sd, multiplies the sum.
 // They run in the order opposite to the row pass that follows: what was read last (and may still be
 // in L2) is read first there.  The two halves of a chunk have their own warps and barriers, so one
 // is weighed while the other is multiplied.
@@ -192,7 +213,7 @@ __device__ __forceinline__ void states_of_segment(const CUtensorMap& tmB, const 
     __syncwarp();
   } else {  // ---- weights: a row of a half chunk, 32 columns a thread ----
     const int half = warp >> 3, r = half * 64 + (tid & 63), c0 = ((tid >> 6) & 3) * 32;
-    const float g2 = log2_decay(p.log_decay, h);
+    const float g2 = log2_decay(p.log_decay, h), mid = middle(g2, r_end - r_begin, p.e);
     // the sum: row (TMEM lane) rs, columns cs .. cs + 31
     const int rs = tid & 127, cs = (tid >> 7) * 32;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -213,7 +234,7 @@ __device__ __forceinline__ void states_of_segment(const CUtensorMap& tmB, const 
       const int row = chunk_row(i) + r;
       const bool valid = row < r_end;
       const int m = p.reverse ? row - r_begin + 1 - p.e : r_end - p.e - row;
-      const float w = valid ? p.sd * exp2f(g2 * (float)m) : 0.f;
+      const float w = valid ? exp2f(g2 * ((float)m - mid)) : 0.f;
       ok = wait(kFull + s, (i / kStStages) & 1);
       if (!ok) break;
       uint8_t* hi = sm + s * 2 * kTile;
@@ -247,6 +268,9 @@ __device__ __forceinline__ void states_of_segment(const CUtensorMap& tmB, const 
       if (group > 0 && (nc - 1) % kFlush < kLate) flush(group - 1);
       flush(group);
       float* dst = state_of(p) + rs * 4;
+      const float all = p.sd * exp2f(g2 * mid);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) sum[j] *= all;
       if (rs < p.D) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -305,7 +329,7 @@ constexpr uint32_t kColP = 0, kColIn = 128, kColSt = 256, kColAdd = 384;
 //   add = b^T c;  in = P c;  st = a S                                         (warp 17)
 //   out = in + si L^(t+e) st -> over c's tile -> global                       (warps 0-7, 18)
 // (over c's, which the next product needs last: over a's, the next load of a came 1,100 clk late)
-//   S = L^rows S + add, in registers (half a row a thread), bf16 copy for a S (warps 8-15)
+//   S = L^rows S + sd add, in registers (half a row a thread), bf16 copy for a S (warps 8-15)
 template <bool kReverse, bool kOutF32>
 __device__ __forceinline__ void rows_of_segment(const CUtensorMap& tmA, const CUtensorMap& tmB,
                                                 const CUtensorMap& tmC, const CUtensorMap& tmOut,
@@ -653,11 +677,11 @@ __device__ __forceinline__ void rows_of_segment(const CUtensorMap& tmA, const CU
       const int rows = min(kRows, r_end - chunk_row(i));
       const int t = kReverse ? rows - 1 - r : r;
       const bool valid = r < rows;
-      // The weight is rounded to bf16 before the product is: one rounding more on the way through the
-      // carried state (two of b, the state's copy, the output: 2^-8 / sqrt(3) * sqrt(4) = 4.5e-3 at
-      // most in the mean square), for a quarter of the instructions.
-      const __nv_bfloat162 w2 = __float2bfloat162_rn(valid ? p.sd * ex2(g2 * (float)(rows - t - p.e))
-                                                           : 0.f);
+      // x w is rounded to bf16 once, on the way through the carried state (with the state's copy and
+      // the output three roundings: 2^-8 / sqrt(3) * sqrt(3) = 3.9e-3 at most in the mean square)
+      const float mid = middle(g2, rows, p.e);
+      const Weight w(valid ? ex2(g2 * ((float)(rows - t - p.e) - mid)) : 0.f);
+      const float all = p.sd * ex2(g2 * mid);
       uint8_t* tb = sm + s * kRwStage + kTile;
       ok = wait(kScores, i & 1) && wait(kCFull + s, (i >> 1) & 1);
       if (!ok) break;
@@ -668,8 +692,8 @@ __device__ __forceinline__ void rows_of_segment(const CUtensorMap& tmA, const CU
           uint4* q1 = reinterpret_cast<uint4*>(tb + sw128_offset(r, c + 8, kRows));
           uint4 x = *q0, y = *q1;
           if (!valid) x = y = make_uint4(0, 0, 0, 0);
-          *q0 = mul8(x, w2);
-          *q1 = mul8(y, w2);
+          *q0 = mul8(x, w);
+          *q1 = mul8(y, w);
         }
       }
       if (!valid)  // padding may hold anything, and P's zeros must not meet it
@@ -680,7 +704,7 @@ __device__ __forceinline__ void rows_of_segment(const CUtensorMap& tmA, const CU
       mbar_arrive(&bars[kBReady]);
       if (last) break;
       const float keep = ex2(g2 * (float)rows);
-      const uint64_t keep2 = f2_pack(keep, keep);
+      const uint64_t keep2 = f2_pack(keep, keep), all2 = f2_pack(all, all);
       // also waits until a S of this chunk has read the copy
       ok = wait(kAddFull, i & 1) && wait(kOFull, i & 1);
       if (!ok) break;
@@ -691,7 +715,8 @@ __device__ __forceinline__ void rows_of_segment(const CUtensorMap& tmA, const CU
         tmem_ld16(tmem + lanes + kColAdd + c0 + q * 16, v);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          S[q * 8 + j] = f2_fma(keep2, S[q * 8 + j], f2_bits(v[2 * j], v[2 * j + 1]));
+          S[q * 8 + j] = f2_fma(keep2, S[q * 8 + j],
+                                f2_mul(all2, f2_bits(v[2 * j], v[2 * j + 1])));
       }
       tc_fence_before();
       publish();
