@@ -4,9 +4,12 @@
 // and up are copied.  The gradient is the same turn by -a.
 //
 // Angles: a float holds pos * freq only to 2^-24 of its value, which at position 10^6 is 0.06
-// radians.  So a frequency is kept as a 64-bit fraction of a turn, and pos * freq modulo one turn is
-// an integer product that wraps: exact for every 64-bit position.  The wrapped turn's upper 32 bits
-// give the angle to 1.5e-9 radians, and sincospif its sine and cosine.
+// radians.  So a frequency is kept as a 64-bit fraction of a turn, within 2 units of 2^-64, and
+// pos * freq modulo one turn is an integer product that wraps: off by at most 2 |pos| 2^-64 turns
+// (7.5e-7 radians at position 2^40; a fraction of fp64's 53 bits was 8.9e-5 off there).  Of the
+// wrapped turn the nearest quarter is taken off, so what becomes a float is at most an eighth of a
+// turn: 2.3e-8 radians, a quarter of what a whole turn's float loses.  sincospif gives its sine and
+// cosine, and the quarter turns them.
 //
 // Bound by memory: every row is read and written once.  A thread owns eight pairs of one token:
 // it forms their sines and cosines once, in registers, and applies them to every head of both
@@ -51,9 +54,16 @@ struct Params {
   int heads_per_block;
 };
 
+// x modulo 1 in units of 2^-64, nearest: x - rint(x) is exact, and so is its product.
+__device__ __forceinline__ unsigned long long fraction64(double x) {
+  return static_cast<unsigned long long>(__double2ll_rn((x - rint(x)) * 18446744073709551616.0));
+}
+// freq / (2 pi) modulo one turn.  The constant and its product with freq are both sums of two doubles,
+// good to 2^-105 of freq: a fraction's own 64 bits decide.
 __device__ __forceinline__ unsigned long long turn_fraction(double freq) {
-  const double t = freq * 0.15915494309189533577;  // 1 / (2 pi)
-  return static_cast<unsigned long long>((t - floor(t)) * 18446744073709551616.0);
+  constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;  // 1 / (2 pi)
+  const double hi = freq * kHi, lo = fma(freq, kHi, -hi) + freq * kLo;
+  return fraction64(hi) + fraction64(lo);
 }
 __device__ __forceinline__ long long position(const Params& p, int axis, int b, int i) {
   long long x = p.start + (p.add_index ? i : 0);
@@ -68,9 +78,15 @@ __device__ __forceinline__ void turn(const Params& p, int pair, int b, int i, fl
   const int axis = p.axis ? min((int)p.axis[pair], p.axes - 1) : 0;
   const unsigned long long a = static_cast<unsigned long long>(position(p, axis, b, i)) *
                                turn_fraction(p.freq[pair]);
-  // upper half as a signed fraction of half a turn in [-1, 1): angle = pi * x
-  const float x = (float)(int)(a >> 32) * (1.f / 2147483648.f);
-  sincospif(x, &s, &c);
+  const unsigned quarter = (unsigned)((a + (1ull << 61)) >> 62);
+  // what is left, in [-1/8, 1/8] turns: its upper half, in units of 2^-31 half turns
+  const int rest = (int)((a - ((unsigned long long)quarter << 62)) >> 32);
+  float cr, sr;
+  sincospif((float)rest * (1.f / 2147483648.f), &sr, &cr);
+  c = quarter & 1 ? sr : cr;
+  s = quarter & 1 ? cr : sr;
+  if (quarter == 1 || quarter == 2) c = -c;
+  if (quarter >= 2) s = -s;
   c *= p.scale;
   s *= p.scale * p.sign;
 }

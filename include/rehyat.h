@@ -329,10 +329,11 @@ typedef struct {
  *   pos   the position of token i of sequence b on axis `axis[p]` (axis [R/2] bytes < axes, or NULL
  *         for axis 0), at pos[axis*pos_axis + b*pos_batch + i*pos_token] (int32, or int64 with
  *         pos64 != 0), to which `start` and, with add_index != 0, i are added; pos NULL: 0.
- * Angles are exact modulo a turn for every 64-bit position.  Any even 2 <= R <= D; no alignment
- * or stride rule beyond the element's (16-byte aligned rows with R, D multiples of 16 move whole
- * vectors; an input may be expanded, an output not).  q_out/k_out may be q/k (same strides); then nothing is copied.  Enqueued on `stream`;
- * allocates nothing. */
+ * Positions are 64-bit: an angle is off by at most 2 |position| 2^-64 turns (7.5e-7 radians at
+ * 2^40, 7.7e-4 at 2^50) and 2.5e-8 radians.  Any even 2 <= R <= D; no alignment or stride rule
+ * beyond the element's (16-byte aligned rows with R, D multiples of 16 move whole vectors; an input
+ * may be expanded, an output not).  q_out/k_out may be q/k (same strides); then nothing is copied.
+ * Enqueued on `stream`; allocates nothing. */
 typedef struct {
   int B, n, Hq, Hk, D, R;
   int interleaved, inverse;
