@@ -22,7 +22,7 @@
 #pragma once
 
 #include "decay.cuh"
-#include "sm100.cuh"
+#include "sm100_rows.cuh"
 
 namespace rehyat {
 namespace decay {
