@@ -4,7 +4,6 @@
 #pragma once
 
 #include <atomic>
-#include <initializer_list>
 
 #include "decay.cuh"
 #include "decay_bf16.cuh"
@@ -38,7 +37,7 @@ int check_decay(const DecayDims& a) {
   return REHYAT_OK;
 }
 
-// A strided [B, heads, N, D] tensor: aligned, whole 16-byte strides, rows that do not overlap.
+// A strided [B, heads, N, D] tensor: aligned, whole 16-byte strides of at least a row.
 int check_rows(const char* what, const rehyat_rows& s, const DecayDims& a, int heads) {
   const int el = a.dt == REHYAT_BF16 ? 2 : 4, D = a.D;
   if (a.N == 0) return REHYAT_OK;
@@ -296,10 +295,123 @@ void set_out(Pass& p, const rehyat_rows& o) {
   p.ob = o.batch; p.oh = o.head; p.on = o.row;
 }
 
-// CTAs that share a row write their part of it while others may still read theirs.
-int check_apart(const char* what, const void* out, std::initializer_list<const void*> others) {
-  for (const void* p : others)
-    if (p && p == out) return fail(REHYAT_ERR_ARG, "%s may not be another argument", what);
+// ---- where the arguments of a call lie ----
+// Bytes of one argument: runs of `run` bytes, repeated along up to three dimensions in ascending
+// order of their strides.
+struct Place {
+  const char* what = nullptr;
+  bool written = false;
+  intptr_t p = 0;
+  long long run = 0, size[3], stride[3];
+  int dims = 0;
+
+  // Bytes from the first to the last of the runs along the first n dimensions.
+  __int128 extent(int n) const {
+    __int128 e = run;
+    for (int i = 0; i < n; ++i) e += (__int128)(size[i] - 1) * stride[i];
+    return e;
+  }
+  // No byte is reached twice; sufficient, and true of every slice, transpose or stack of a dense
+  // tensor.
+  bool apart() const {
+    for (int i = 0; i < dims; ++i)
+      if (stride[i] < extent(i)) return false;
+    return true;
+  }
+};
+Place place(const char* what, const void* p, long long bytes, bool written) {
+  Place a;
+  a.what = what;
+  a.written = written;
+  a.p = reinterpret_cast<intptr_t>(p);
+  a.run = p ? bytes : 0;
+  return a;
+}
+// Runs of `bytes`; counts and strides (in bytes) of three dimensions in any order.
+Place place(const char* what, const void* p, long long bytes, const long long (&n)[3],
+            const long long (&stride)[3], bool written) {
+  Place a = place(what, p, bytes, written);
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] == 0) a.run = 0;
+    if (n[i] <= 1 || (stride[i] == 0 && !written)) continue;  // (an expanded input)
+    long long st = stride[i];
+    if (st < 0) {
+      a.p += (intptr_t)(st * (n[i] - 1));
+      st = -st;
+    }
+    int at = a.dims++;
+    for (; at > 0 && a.stride[at - 1] > st; --at) {
+      a.stride[at] = a.stride[at - 1];
+      a.size[at] = a.size[at - 1];
+    }
+    a.stride[at] = st;
+    a.size[at] = n[i];
+  }
+  int merged = 0;  // innermost dimensions that continue the run
+  while (merged < a.dims && a.stride[merged] == a.run) a.run *= a.size[merged++];
+  for (int i = merged; i < a.dims; ++i) {
+    a.stride[i - merged] = a.stride[i];
+    a.size[i - merged] = a.size[i];
+  }
+  a.dims -= merged;
+  return a;
+}
+Place place(const char* what, const rehyat_rows& t, int B, int heads, int N, int D, int el,
+            bool written) {
+  return place(what, t.p, (long long)D * el, {B, heads, N},
+               {t.batch * el, t.head * el, t.row * el}, written);
+}
+
+// Whether two arguments have a byte in common: whether d = (second's address - first's) is a
+// difference of a byte of the first and one of the second, sum over the strides of both of (i - j)
+// stride + (x - y), i < size and x < run in the first, j and y in the second.  From the largest stride
+// down, what is left of d has to be within reach of the smaller ones, which leaves two or three
+// values of i - j where strides are nested; where one argument's runs cover many strides of the
+// other, a value in the middle decides.  Never true without a common byte.
+bool meet(const Place& a, int na, const Place& b, int nb, __int128 d) {
+  const __int128 ra = a.extent(na) - 1, rb = b.extent(nb) - 1;
+  if (d > ra || d < -rb) return false;
+  if (na == 0 && nb == 0) return true;
+  const long long sa = na ? a.stride[na - 1] : -1, sb = nb ? b.stride[nb - 1] : -1;
+  const long long s = sa > sb ? sa : sb;
+  if (s <= 0) return false;  // (a written dimension expanded: refused before)
+  const int ma = sa == s ? na - 1 : na, mb = sb == s ? nb - 1 : nb;
+  const __int128 la = a.extent(ma) - 1, lb = b.extent(mb) - 1;  // reach of what is left
+  auto floor_div = [](__int128 x, __int128 y) { return x / y - (x % y < 0); };
+  __int128 lo = -floor_div(la - d, s), hi = floor_div(d + lb, s);
+  const __int128 most = sa == s ? a.size[na - 1] - 1 : 0, least = sb == s ? 1 - b.size[nb - 1] : 0;
+  if (lo < least) lo = least;
+  if (hi > most) hi = most;
+  const __int128 mid = lo + (hi - lo) / 2;
+  for (__int128 e = lo; e <= hi; ++e) {
+    if (e == lo + 2 && e < mid) e = mid;
+    if (e > mid && e < hi - 1) e = hi - 1;
+    if (meet(a, ma, b, mb, d - e * s)) return true;
+  }
+  return false;
+}
+
+// No written argument reaches a byte of its own twice, or a byte of another argument: CTAs write
+// their parts while others still read or write theirs.
+template <int n>
+int check_places(const Place (&a)[n]) {
+  __int128 end[n];
+  for (int i = 0; i < n; ++i) {
+    if (a[i].run && a[i].written && !a[i].apart())
+      return fail(REHYAT_ERR_ARG, "%s: its rows overlap one another", a[i].what);
+    end[i] = a[i].p + a[i].extent(a[i].dims);
+  }
+  for (const bool same : {true, false})
+    for (int i = 1; i < n; ++i)
+      for (int j = 0; j < i; ++j) {
+        if (!a[i].run || !a[j].run || !(a[i].written || a[j].written)) continue;
+        const Place& w = a[i].written ? a[i] : a[j];
+        if (same && a[i].p == a[j].p)
+          return fail(REHYAT_ERR_ARG, "%s may not be another argument", w.what);
+        if (!same && a[i].p < end[j] && a[j].p < end[i] &&
+            meet(a[i], a[i].dims, a[j], a[j].dims, (__int128)a[j].p - a[i].p))
+          return fail(REHYAT_ERR_ARG, "%s overlaps %s", w.what, a[i].written ? a[j].what : a[i].what);
+      }
   return REHYAT_OK;
 }
 
@@ -366,10 +478,19 @@ int rehyat_rotary(const rehyat_rotary_args* args, void* stream) {
                     size[j % 3], a.D);
     }
   }
-  if (a.Hk) {
-    RH_TRY(check_apart("q_out", a.q_out.p, {a.k.p, a.k_out.p}));
-    RH_TRY(check_apart("k_out", a.k_out.p, {a.q.p}));
-  }
+  // an input that is its own output is looked at once, as the output
+  rehyat_rows q = a.q, k = a.k;
+  if (q.p == a.q_out.p) q.p = nullptr;
+  if (k.p == a.k_out.p) k.p = nullptr;
+  const int pe = a.pos64 ? 8 : 4;
+  RH_TRY(check_places({place("q_out", a.q_out, a.B, a.Hq, a.n, a.D, el, true),
+                       place("k_out", a.k_out, a.B, a.Hk, a.n, a.D, el, true),
+                       place("q", q, a.B, a.Hq, a.n, a.D, el, false),
+                       place("k", k, a.B, a.Hk, a.n, a.D, el, false),
+                       place("freq", a.freq, a.R * 4LL, false),
+                       place("axis", a.axis, a.R / 2, false),
+                       place("pos", a.pos, pe, {a.axes, a.B, a.n},
+                             {a.pos_axis * pe, a.pos_batch * pe, a.pos_token * pe}, false)}));
   p.B = a.B; p.n = a.n; p.D = a.D; p.R = a.R;
   p.interleaved = a.interleaved; p.copy_tail = !in_place && a.R < a.D;
   p.freq = a.freq; p.axis = a.axis; p.pos = a.pos; p.pos64 = a.pos64; p.axes = a.axes;
@@ -429,7 +550,17 @@ int rehyat_decay_forward(const rehyat_decay_forward_args* args, void* stream) {
   RH_TRY(check_states("S_last", a.S_last));
   const DecayPlan pl = plan_decay(d, false, a.lengths != nullptr, a.S_last != nullptr);
   RH_TRY(check_scratch(pl, a.workspace, a.ws_bytes));
-  RH_TRY(check_apart("out", a.out.p, {a.q.p, a.k.p, a.v.p}));
+  const int el = d.dt == REHYAT_BF16 ? 2 : 4;
+  const long long states = 4LL * a.B * a.H * a.D * a.D;
+  RH_TRY(check_places({place("q", a.q, a.B, a.H, a.N, a.D, el, false),
+                       place("k", a.k, a.B, a.Hk, a.N, a.D, el, false),
+                       place("v", a.v, a.B, a.Hk, a.N, a.D, el, false),
+                       place("out", a.out, a.B, a.H, a.N, a.D, el, true),
+                       place("S0", a.S0 == a.S_last ? nullptr : a.S0, states, false),
+                       place("S_last", a.S_last, states, true),
+                       place("log_decay", a.log_decay, 4LL * a.H, false),
+                       place("lengths", a.lengths, 4LL * a.B, false),
+                       place("workspace", a.workspace, pl.total, true)}));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int group = a.H / a.Hk;
   Pass p = decay_pass(d, a.log_decay, a.lengths, pl.cut, static_cast<uint8_t*>(a.workspace) + pl.fwd);
@@ -464,10 +595,21 @@ int rehyat_decay_backward(const rehyat_decay_backward_args* args, void* stream) 
   RH_TRY(check_states("dS0", a.dS0));
   const DecayPlan pl = plan_decay(d, true, a.lengths != nullptr, a.dS0 != nullptr);
   RH_TRY(check_scratch(pl, a.workspace, a.ws_bytes));
-  RH_TRY(check_apart("dq", a.dq.p, {a.q.p, a.k.p, a.v.p, a.dout.p}));
-  RH_TRY(check_apart("dk", a.dk.p, {a.q.p, a.k.p, a.v.p, a.dout.p, a.dq.p}));
-  RH_TRY(check_apart("dv", a.dv.p, {a.q.p, a.k.p, a.v.p, a.dout.p, a.dq.p, a.dk.p}));
-  RH_TRY(check_apart("dS0", a.dS0, {a.S0, a.dS_last}));
+  const int el = d.dt == REHYAT_BF16 ? 2 : 4;
+  const long long states = 4LL * a.B * a.H * a.D * a.D;
+  RH_TRY(check_places({place("q", a.q, a.B, a.H, a.N, a.D, el, false),
+                       place("k", a.k, a.B, a.Hk, a.N, a.D, el, false),
+                       place("v", a.v, a.B, a.Hk, a.N, a.D, el, false),
+                       place("dout", a.dout, a.B, a.H, a.N, a.D, el, false),
+                       place("dq", a.dq, a.B, a.H, a.N, a.D, el, true),
+                       place("dk", a.dk, a.B, a.Hk, a.N, a.D, el, true),
+                       place("dv", a.dv, a.B, a.Hk, a.N, a.D, el, true),
+                       place("S0", a.S0, states, false),
+                       place("dS_last", a.dS_last, states, false),
+                       place("dS0", a.dS0, states, true),
+                       place("log_decay", a.log_decay, 4LL * a.H, false),
+                       place("lengths", a.lengths, 4LL * a.B, false),
+                       place("workspace", a.workspace, pl.total, true)}));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const int group = a.H / a.Hk;
@@ -542,7 +684,14 @@ int rehyat_decay_step(const rehyat_decay_step_args* args, void* stream) {
   RH_TRY(check_states("state", a.state));
   if (a.pool < 1 || (!a.slots && a.pool < a.B))
     return fail(REHYAT_ERR_ARG, "a pool of %d states for %d sequences", a.pool, a.B);
-  RH_TRY(check_apart("out", a.out.p, {a.q.p, a.k.p, a.v.p}));
+  const int el = d.dt == REHYAT_BF16 ? 2 : 4;
+  RH_TRY(check_places({place("q", a.q, a.B, a.H, 1, a.D, el, false),
+                       place("k", a.k, a.B, a.Hk, 1, a.D, el, false),
+                       place("v", a.v, a.B, a.Hk, 1, a.D, el, false),
+                       place("out", a.out, a.B, a.H, 1, a.D, el, true),
+                       place("state", a.state, 4LL * a.pool * a.H * a.D * a.D, true),
+                       place("log_decay", a.log_decay, 4LL * a.H, false),
+                       place("slots", a.slots, 4LL * a.B, false)}));
   rehyat::decay::StepParams p{};
   const int group = a.H / a.Hk;
   p.q = rows_of(a.q, 1);

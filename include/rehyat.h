@@ -313,8 +313,11 @@ int rehyat_segment_attend(rehyat_dims d, rehyat_dtype dt, int T, int frame_token
  * strides: rehyat_rows gives the elements between two sequences, two heads and two rows of a
  * [B, heads, N, D] tensor whose D elements are contiguous, so a [B, N, heads, D] projection or a
  * slice of a packed qkv is read in place.  Unless stated, pointers and strides are multiples of 16
- * bytes (the stride of a dimension of size 1 is not looked at), and a written tensor overlaps no
- * other argument.  `dtype` (a rehyat_dtype) is the type of all rows. */
+ * bytes (the stride of a dimension of size 1 is not looked at), and a written tensor overlaps neither
+ * itself nor another argument: a call whose addresses, sizes and strides show an overlap is refused,
+ * and so is an output whose strides are not nested (each at least the extent of the smaller ones).
+ * Tensors that lie between one another's rows, as slices of one buffer do, are fine.  `dtype` (a
+ * rehyat_dtype) is the type of all rows. */
 typedef struct {
   void* p;
   long long batch, head, row;
