@@ -719,6 +719,11 @@ def _call(index: int, fn, block: bytes) -> None:
         _check(status)
 
 
+# A tensor of the caller's that a call wrote to: a graph that saved it for its backward pass then says
+# so there, instead of taking the new values for the old.
+_wrote = torch.autograd.graph.increment_version
+
+
 def _four(t: torch.Tensor, what: str):
     shape = t.shape
     if len(shape) != 4:
@@ -828,6 +833,7 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, freq: torch.Tensor, *,
             raise ValueError("all tensors must be on the same CUDA device")
         pp = pos.data_ptr()
     ap = 0 if axis is None else _small(axis, torch.uint8, index, (half,), "axis")
+    given = [t for t in (q_out, k_out) if t is not None]
     Hk, ka, ko = 0, _NO_ROWS, _NO_ROWS
     if k is not None:
         Hk = _four(k, "k")[1]
@@ -841,6 +847,8 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, freq: torch.Tensor, *,
     _call(index, lib.rehyat_rotary, _ROTARY.pack(
         B, n, H, Hk, D, 2 * half, interleaved, inverse, axes, pos64, add, code, pa, pb, pn, start,
         fp, ap, pp, *qa, *ka, *qo, *ko, scale))
+    if given:
+        _wrote(given)
     return q_out if k is None else (q_out, k_out)
 
 
@@ -883,12 +891,14 @@ def decay_forward(q, k, v, log_decay, *, scale: float = 1.0, lengths: torch.Tens
     gp = _small(log_decay, torch.float32, index, (H,), "log_decay")
     lp = 0 if lengths is None else _small(lengths, torch.int32, index, (B,), "lengths")
     sp = 0 if state is None else _small(state, torch.float32, index, square, "state")
+    given = [] if out is None else [out]
     if out is None:
         out = torch.empty_like(q)
     oa = _rows(out, dtype, index, shape, "out")
     last, fp = None, 0
     if isinstance(final_state, torch.Tensor):
         last = final_state
+        given.append(last)
         fp = _small(last, torch.float32, index, square, "final_state")
     elif final_state:
         last = torch.empty(square, dtype=torch.float32, device=q.device)
@@ -896,6 +906,8 @@ def decay_forward(q, k, v, log_decay, *, scale: float = 1.0, lengths: torch.Tens
     ws = _scratch(decay_workspace_size(B, H, Hk, N, D), q.device, workspace)
     _call(index, lib.rehyat_decay_forward, _DECAY_FORWARD.pack(
         B, H, Hk, N, D, code, *qa, *ka, *va, *oa, gp, lp, sp, fp, ws.data_ptr(), ws.numel(), scale))
+    if given:
+        _wrote(given)
     return out if last is None else (out, last)
 
 
@@ -949,9 +961,11 @@ def decay_step(q, k, v, log_decay, state, *, scale: float = 1.0,
     gp = _small(log_decay, torch.float32, index, (H,), "log_decay")
     sp = _small(state, torch.float32, index, (pool, H, D, D), "state")
     lp = 0 if slots is None else _small(slots, torch.int32, index, (B,), "slots")
+    given = state if out is None else (state, out)
     if out is None:
         out = torch.empty_like(q)
     _call(index, lib.rehyat_decay_step, _DECAY_STEP.pack(
         B, H, Hk, D, pool, code, *qa, *ka, *va, *_rows(out, dtype, index, shape, "out"), gp, sp, lp,
         scale))
+    _wrote(given)
     return out
