@@ -742,7 +742,8 @@ def rotary_frequencies(R: int, *, base: float = 10000.0, scaling: str | None = N
                         factor and the fastest not at all;
       scaling "yarn":   pairs that make at least turns[0] turns over `original_length` positions are
                         kept, those with at most turns[1] divided by the factor, a linear ramp over
-                        the pair index between; values times 0.1 ln(factor) + 1."""
+                        the pair index between (from pair 0 at the earliest); values times
+                        0.1 ln(factor) + 1."""
     if R < 2 or R % 2:
         raise ValueError(f"R={R} must be even and positive")
     if not factor >= 1.0 or not base > 1.0:
@@ -762,7 +763,8 @@ def rotary_frequencies(R: int, *, base: float = 10000.0, scaling: str | None = N
         lo, hi = (R * math.log(original_length / (t * 2 * math.pi)) / (2 * math.log(base))
                   for t in turns)
         lo, hi = max(math.floor(lo), 0), min(math.ceil(hi), R - 1)
-        keep = 1 - ((p - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        # (hi <= 0: no pair makes more than turns[1] turns)
+        keep = 1 - ((p - lo) / max(hi - lo, 1e-3)).clamp(0, 1) if hi > 0 else torch.zeros_like(p)
         freq = freq * keep + freq / factor * (1 - keep)
         scale = 0.1 * math.log(factor) + 1.0
     elif scaling not in (None, "ntk"):
