@@ -404,3 +404,60 @@ def test_refuses(dev):
     for kw in (dict(state=p["S0"][:1]), dict(slots=i32(1)), dict(out=q)):
         with pytest.raises(ValueError):
             rb.decay_step(*one, g, **dict(dict(state=p["S0"]), **kw))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("B,H,Hk,N", [(33, 1, 1, 1000), (100, 2, 1, 500), (256, 1, 1, 300)], ids=str)
+def test_padded_batches_of_many_sequences(dev, dtype, B, H, Hk, N):
+    """As many sequences as one warp finds the segments of, several to a lane: long ones, runs of
+    empty ones (the first 32 among them, and the last), one row, and a chunk's border."""
+    lengths = [0] * 32 + [(N, 1, 128, 129, 64, 0, 0, 0, N - 1, 300)[i % 10] for i in range(B - 32)]
+    if B > 64:
+        lengths[60:100] = [0] * 40
+        lengths[2], lengths[-1] = N, 0
+    n = [min(x, N) for x in lengths]
+    p = problem(dev, dtype, B, H, Hk, N, 32, True, seed=40 + B, decays=[-0.03, -0.2][:H])
+    L = torch.tensor(lengths, dtype=torch.int32, device=dev)
+    kw = dict(scale=0.2, lengths=L, state=p["S0"])
+    out, last = rb.decay_forward(p["q"], p["k"], p["v"], p["g"], final_state=True, **kw)
+    only = rb.decay_forward(p["q"], p["k"], p["v"], p["g"], **kw)
+    g = rb.decay_backward(p["q"], p["k"], p["v"], p["g"], p["dout"], dfinal=p["dS"], **kw)
+    rb.sync_status(dev)
+    want = {x: [] for x in ("out", "dq", "dk", "dv", "last", "dstate")}
+    for b in range(B):
+        kv = [np.zeros((Hk, n[b], 32)) for _ in range(2)]
+        for h in range(H):
+            x = [head(p, c, b, h, n[b]) for c in ("q", "k", "v", "dout")]
+            S0, dS, gh = f64(p["S0"][b, h]), f64(p["dS"][b, h]), float(p["g"][h])
+            o, S = SO.decay_forward(*x[:3], gh, S0, 0.2)
+            dq, dk, dv, d0 = SO.decay_backward(*x[:3], gh, x[3], S0, dS, 0.2)
+            kv[0][h * Hk // H] += dk
+            kv[1][h * Hk // H] += dv
+            for name, w in (("out", o), ("dq", dq), ("last", S), ("dstate", d0)):
+                want[name].append(w)
+        want["dk"] += list(kv[0])
+        want["dv"] += list(kv[1])
+    for name, x in (("out", out), ("out", only), ("dq", g["dq"]), ("dk", g["dk"]), ("dv", g["dv"])):
+        # padding is zero and left out: its zeros would shrink the root mean square that one value's
+        # error is measured in (of 33,000 rows 1,000 are valid: by sqrt(33))
+        assert not any(bool(x[b, :, n[b]:].any()) for b in range(B)), name
+        rows_ = torch.cat([x[b, h, :n[b]] for b in range(B) for h in range(x.shape[1])])
+        close(rows_, np.concatenate(want[name]), REL[dtype], name)
+    for name, x in (("last", last), ("dstate", g["dstate"])):
+        close(x, np.stack(want[name]).reshape(x.shape), REL_STATE[dtype], name)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("H,Hk,N", [(2, 1, 700), (2, 2, 50), (150, 150, 300)], ids=str)
+@pytest.mark.parametrize("have", ["S0", "dS"])
+def test_gradients_with_one_of_the_states(dev, dtype, H, Hk, N, have):
+    """A state before without a gradient of the last, and the other way round: only one of the passes
+    has something carried in (one segment a sequence, or several)."""
+    p = problem(dev, dtype, 1, H, Hk, N, 64, True, seed=50 + N)
+    for name in ("S0", "dS"):
+        if name != have:
+            p[name] = None
+    g = rb.decay_backward(p["q"], p["k"], p["v"], p["g"], p["dout"], scale=0.125, state=p["S0"],
+                          dfinal=p["dS"])
+    rb.sync_status(dev)
+    check_backward(p, g, 0.125)
