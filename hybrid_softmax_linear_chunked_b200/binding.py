@@ -883,7 +883,10 @@ def decay_forward(q, k, v, log_decay, *, scale: float = 1.0, lengths: torch.Tens
     lengths [B] int32: sequence b is its first lengths[b] rows, the others are padding (not read
     into any result, zero in the output).  state [B,H,D,D] fp32: from the rows before.
     final_state True: returns (out, the state after the last row [B,H,D,D] fp32), which
-    `decay_step` or the next call goes on from; a tensor: written there (it may be `state`)."""
+    `decay_step` or the next call goes on from; a tensor: written there (it may be `state`).  In bf16
+    asking for it changes the last bits of `out` (the sums between segments are then finer).
+    Tensors of rows may have any strides of at least D and whole 16 bytes (none expanded); an output
+    that overlaps itself or another argument is refused."""
     lib = _lib or load()
     B, H, Hk, N, D = _decay_sizes(q, k)
     dtype, code, index = _typed(q)

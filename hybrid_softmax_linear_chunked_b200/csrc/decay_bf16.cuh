@@ -1,21 +1,23 @@
 // Linear attention with a decay per head on the tensor cores (bf16, D <= 128): the two passes of
 // decay.cuh over 128-row chunks.
 //
-// A chunk of the row pass moves 128 KB of HBM (a, b, c in, out) for four 128^3 products: 5,600 clk of
-// one SM's share of the measured copy rate against 2,048 clk of the tensor pipe.  What it comes to,
-// about 5,000 clk, is shared memory: operands that the products read from it (224 KB), the copies in
-// (96), the weighting of b (64), the state's copy (32) and the output's staging (64) are 480 KB, 3,840
-// clk at 128 bytes a clk.  The 480x832 5 s prompt (12 heads, 32,760 rows, D = 128): states 46 us
-// (4.4 TB/s), rows 74 us (5.4 TB/s).  Long runs are held at 1.45-1.65 GHz by the board's power limit.
+// A chunk of the row pass moves 128 KB of HBM (a, b, c in, out) for four 128^3 products: 3.0 us of one
+// SM's share of the measured copy rate, against 1.1 us of the tensor pipe at 1.9 GHz.  The 480x832 5 s
+// prompt (12 heads, 32,760 rows, D = 128; 402 MB): rows 74-79 us, 5.1 to 5.4 TB/s or 0.78 to 0.83 of the
+// copy rate, 3.5-3.7 us a chunk.  So HBM bounds it first, with each CTA's start and the chain from one
+// chunk to the next on top: of the cycles, shared memory is busy in 64 % (products 27, warps 21, copies
+// 16) and the tensor pipe in 31 %.  What a prompt takes beyond that is the states pass, 46 us (4.4 TB/s,
+// k and v read a first time), and the scan.  Long runs are held at 1.45-1.65 GHz by the board's power
+// limit.
 // Not faster: the outputs on eight warps of their own (setmaxnreg shares), runs of chunks that cross
 // from one head into the next, L2 eviction hints, waits by test_wait or with nanosleep.
 // One CTA per SM, two (rows) or three (states) stages of whole chunks, one warp for each thing that
 // waits, short loops (straight-line code of every role at once overran the instruction cache).
 //
 // Rounded to bf16: the weighted scores P, the weighted rows b of the carried state, the state the
-// rows read, and the output; sums, states and powers are fp32.  The states pass multiplies each
-// weighted row in two bf16 parts (16 mantissa bits), so the states between segments and the last
-// state are fp32 sums of terms good to 2^-16.
+// rows read, and the output; sums, states and powers are fp32.  Where the last state is given out, the
+// states pass multiplies each weighted row in two bf16 parts (16 mantissa bits), so that state and those
+// between segments are fp32 sums of terms good to 2^-16; where only the row pass reads them, in one.
 //
 // Narrow heads (D < 128) run on the same tiles: columns at and past D load as zeros (the tensor map
 // ends there) and are not stored, and the products' depth and width stop at D rounded up to 16.

@@ -363,8 +363,13 @@ int rehyat_rotary(const rehyat_rotary_args* args, void* stream);
  * infinity in a row stays within its sequence and the heads that share its k and v; there it
  * reaches the rows after it, the states, and earlier rows of its own chunk (128 rows in bf16, 64
  * in fp32); in the gradients any row.
- * D a multiple of 8 up to 128; B*H up to 65535; N may be 0.  bf16: tensor-core products with fp32 accumulation
- * (the states are summed from two-part products, to fp32 accuracy).  fp32: CUDA cores.
+ * D a multiple of 8 up to 128; B*H up to 65535; N may be 0.
+ * bf16: tensor-core products with fp32 accumulation.  Rounded to bf16 on the way: the weighted scores,
+ * the weighted rows of the carried state, the state as the rows read it, and the rows written
+ * (together within 0.005 of a result's norm, typically 0.0025).  States given out are fp32 sums of
+ * terms good to 2^-16.  Where none is asked for (S_last, dS0 NULL), the sums between segments are
+ * taken in one bf16 part, so the last bits of the other outputs depend on whether one is.
+ * fp32: CUDA cores.
  * rehyat_decay_workspace_size: device scratch that the forward (backward = 0) or the gradients
  * need for these sizes. */
 int rehyat_decay_workspace_size(int B, int H, int Hk, int N, int D, int backward, size_t* bytes);
