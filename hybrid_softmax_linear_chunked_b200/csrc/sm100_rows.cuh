@@ -42,10 +42,10 @@ __device__ __forceinline__ void tma_store_4d_chk(int site, const CUtensorMap* ma
       : "memory");
 }
 
-// mma_ss, mma_ts and mma_commit issued by the one lane whose `leader` is non-zero, without a branch: the whole
-// warp computes the descriptors, so they can stay in uniform registers, which the instruction takes
-// its operands from.  Inside an `if (lane == 0)` every operand is moved there one by one, about
-// 130 clk a product instead of the 64 it runs.
+// mma_ss, mma_ts and mma_commit issued by the one lane whose `leader` is non-zero, without a branch:
+// the whole warp computes the descriptors, so they can stay in uniform registers, which the
+// instruction takes its operands from.  Inside an `if (lane == 0)` every operand is moved there one by
+// one, about 130 clk a product instead of the 64 it runs.
 __device__ __forceinline__ void mma_ss_by(uint32_t leader, uint32_t d_tmem, uint64_t a_desc,
                                           uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
